@@ -295,6 +295,151 @@ moe_status moe_layer_forward(const moe_config *cfg, const void *x, const void *W
                              float *f, float *p_mean, float *aux_loss,
                              void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- the trainable gate ------------------------------------------------ */
+
+/* Score functions of moe_route: softmax over the N logits, or the logistic
+ * function of each logit by itself. */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+
+/* Routing of given logits (moe_route) and its gradient (moe_route_backward). */
+typedef struct moe_route_config {
+    int64_t T;            /* tokens, >= 0; T * k < 2^31 */
+    int64_t ld;           /* elements between the logits of two tokens, >= N */
+    int32_t N;            /* experts, 1..256 */
+    int32_t k;            /* experts per token, 1..min(N, 8) */
+    int32_t score;        /* MOE_SCORE_* */
+    int32_t renormalize;  /* divide the chosen scores by their sum */
+    int32_t dtype;        /* MOE_F32 or MOE_BF16: logits and their gradient */
+    /* Node-limited routing, in effect when n_groups > 1 and
+     * topk_groups < n_groups: as in moe_config, but with a node's score the
+     * sum of its group_top largest ranking values (1 <= group_top <=
+     * N / n_groups).  0 / 0 / 0: no nodes. */
+    int32_t n_groups;
+    int32_t topk_groups;
+    int32_t group_top;
+    float   scale;        /* factor on every weight, finite */
+} moe_route_config;
+
+/* Bytes of workspace moe_route and moe_route_backward need (0 on an invalid
+ * configuration).  Host only. */
+size_t moe_route_workspace_bytes(const moe_route_config *cfg);
+
+/* Experts and gate weights from logits ("moe communication costs", Router
+ * design, with a score function of the caller's choice and a balancing bias
+ * that takes part in the choice of experts only).
+ *   logits   [T, N] dtype, rows ld elements apart
+ *   bias     [N] fp32 or NULL
+ *   topk_idx [T, k] int32 out, distinct per token, best first
+ *   topk_w   [T, k] fp32 out
+ *   p_mean   [N] fp32 out or NULL: mean over tokens of s_e / sum_e s_e
+ * With s = softmax(l) or 1 / (1 + exp(-l)), an expert's ranking value is
+ * s_e + bias_e, or l_e itself without a bias (the same order, without the
+ * ties that underflow would make); the k largest are chosen, equal values
+ * lowest index first.  Node scores sum s_e + bias_e (or s_e); equal node
+ * scores lowest node first.  Ranking values and node scores are compared as
+ * 64-bit arithmetic orders them.  Weight of slot j: scale * s_{e_j},
+ * divided by the sum of the k chosen scores if `renormalize` (0 when all of
+ * them are switched off).
+ * A logit of -inf (or a bias of -inf) switches the expert off for the token:
+ * it ranks behind every other, lowest index first, -inf logits score 0, and a
+ * node's score leaves it out; a token without any expert left gets the lowest
+ * indices with weight 0 (for a -inf logit) and adds nothing to p_mean.  +inf
+ * counts as the largest finite fp32 value.  A NaN logit or bias counts as
+ * -inf and sets a bit of the status word.
+ * Rows of topk_idx and topk_w beyond T are not written; T = 0 zeroes p_mean. */
+moe_status moe_route(const moe_route_config *cfg, const void *logits, const float *bias,
+                     int32_t *topk_idx, float *topk_w, float *p_mean,
+                     void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gradient of moe_route with respect to the logits, the choice of experts
+ * held fixed (the bias has none).
+ *   logits   as given to moe_route
+ *   topk_idx [T, k] int32 as moe_route wrote them (an index outside [0, N) is
+ *            left out and sets a bit of the status word; an index that occurs
+ *            twice adds up)
+ *   dtopk_w  [T, k] fp32: gradient of topk_w, or NULL (zero)
+ *   dp_mean  [N] fp32: gradient of p_mean, or NULL (zero); for the balance
+ *            loss alpha * N * sum f_i p_i it is alpha * N * f
+ *   dlogits  [T, N] dtype out, rows ld elements apart; must not overlap
+ *            logits.  Switched-off experts get 0. */
+moe_status moe_route_backward(const moe_route_config *cfg, const void *logits,
+                              const int32_t *topk_idx, const float *dtopk_w,
+                              const float *dp_mean, void *dlogits,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gradient of moe_combine; cfg and workspace as for moe_combine.
+ *   dy       [T, d] dtype: gradient of y
+ *   y_perm   [T*k, d] dtype as given to moe_combine (needed for dtopk_w)
+ *   inv_row  [T*k] int32 from moe_dispatch
+ *   topk_w   [T, k] fp32 (needed for dy_perm)
+ *   dy_perm  [T*k, d] dtype out or NULL: row inv_row[t*k+j] = topk_w[t,j] * dy[t];
+ *            rows that no pair names are not written
+ *   dtopk_w  [T, k] fp32 out or NULL: <dy[t], y_perm[inv_row[t*k+j]]> in fp32,
+ *            0 for a dropped pair
+ * At least one output is given; y_perm may be NULL without dtopk_w and topk_w
+ * without dy_perm.  The gradient of y_shared is dy.  (The gradient of
+ * moe_dispatch's row copy is moe_combine with weights of 1.)  dy_perm may be
+ * y_perm itself. */
+moe_status moe_combine_backward(const moe_config *cfg, const void *dy, const void *y_perm,
+                                const int32_t *inv_row, const float *topk_w, void *dy_perm,
+                                float *dtopk_w, void *workspace, size_t workspace_bytes,
+                                void *stream);
+
+/* ---- dense projections ------------------------------------------------- */
+
+/* Activations of moe_linear: z, max(z, 0), z / (1 + e^-z),
+ * z (1 + erf(z / sqrt 2)) / 2, and its tanh approximation
+ * z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2. */
+enum { MOE_LINEAR_NONE = 0, MOE_LINEAR_RELU = 1, MOE_LINEAR_SILU = 2, MOE_LINEAR_GELU = 3,
+       MOE_LINEAR_GELU_TANH = 4 };
+
+typedef struct moe_linear_config {
+    int64_t M;          /* rows (tokens), 0 .. 2^31 - 1 */
+    int64_t ldx;        /* elements between rows of x and dx, >= n_in */
+    int64_t ldy;        /* elements between rows of y and dy, >= n_out */
+    int64_t ldr;        /* elements between rows of residual, >= n_out */
+    int32_t n_in;       /* multiple of 8 (bf16) or 4 (f32), as is ldx; at most 2^20 */
+    int32_t n_out;      /* >= 1, any; at most 2^20 */
+    int32_t act;        /* MOE_LINEAR_* */
+    int32_t dtype;      /* MOE_F32 or MOE_BF16: x, W, preact, dx, dW */
+    int32_t out_dtype;  /* dtype or MOE_F32: y, residual, dy */
+} moe_linear_config;
+
+/* Bytes of workspace for moe_linear (backward = 0), or for moe_linear and
+ * moe_linear_backward (backward = 1); 0 on an invalid configuration.  Host
+ * only. */
+size_t moe_linear_workspace_bytes(const moe_linear_config *cfg, int32_t backward);
+
+/* One dense projection with its epilogue, for the router's logits (out_dtype
+ * MOE_F32) and for the dense and always-on layers next to the routed experts:
+ *   z = x W^T + bias,  y = act(z) + residual
+ *   x        [M, n_in] dtype, rows ldx apart, 16-byte aligned
+ *   W        [n_out, n_in] dtype, 16-byte aligned
+ *   bias     [n_out] fp32 or NULL
+ *   residual [M, n_out] out_dtype, rows ldr apart, or NULL; may be y itself
+ *            (with ldr = ldy)
+ *   y        [M, n_out] out_dtype out, rows ldy apart
+ *   preact   [M, n_out] dtype out or NULL: z, which moe_linear_backward needs
+ *            when there is an activation
+ * Products are summed in fp32 and the epilogue is computed in fp32 with one
+ * rounding to the output type. */
+moe_status moe_linear(const moe_linear_config *cfg, const void *x, const void *W,
+                      const float *bias, const void *residual, void *y, void *preact,
+                      void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gradients of moe_linear.  With dz = dy * act'(preact):
+ *   dy       [M, n_out] out_dtype, rows ldy apart (also the residual's gradient)
+ *   x, W     as given to moe_linear (x needed for dW, W for dx)
+ *   preact   as moe_linear wrote it; NULL without an activation
+ *   dx       [M, n_in] dtype out, rows ldx apart, or NULL: dz W
+ *   dW       [n_out, n_in] dtype out or NULL: dz^T x
+ *   db       [n_out] fp32 out or NULL: the column sums of dz
+ * dz is rounded to dtype for the products (not for db).  At least one output
+ * is given.  M = 0 zeroes dW and db.  dx, dW and db must not overlap inputs. */
+moe_status moe_linear_backward(const moe_linear_config *cfg, const void *dy, const void *x,
+                               const void *W, const void *preact, void *dx, void *dW, float *db,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
 /* Synchronises `stream`, reads and clears the device status word of the
  * workspace.  Returns MOE_OK, MOE_ERR_DEVICE_STATUS or MOE_ERR_TIMEOUT;
  * *detail (if not NULL) receives the raw word (bit meanings in the source). */

@@ -8,7 +8,9 @@ CUDA device is present, the calls raise.
 
 Entry points (same names as the C ABI):
     moe_workspace_bytes, moe_router, moe_dispatch, moe_expert_ffn, moe_combine,
-    moe_layer_forward, moe_check_status, moe_status_string, moe_version.
+    moe_layer_forward, moe_check_status, moe_status_string, moe_version;
+    the trainable gate: moe_route, moe_route_backward, moe_combine_backward;
+    dense projections: moe_linear, moe_linear_backward.
 """
 from __future__ import annotations
 
@@ -24,11 +26,16 @@ MOE_F32, MOE_BF16, MOE_FP8_E4M3 = 0, 1, 2
 MOE_GATE_TOPK_THEN_SOFTMAX, MOE_GATE_SOFTMAX_THEN_TOPK = 0, 1
 MOE_ACT_RELU, MOE_ACT_SWIGLU = 0, 1
 MOE_OVERFLOW_DROP, MOE_OVERFLOW_FALLBACK = 0, 1
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+(MOE_LINEAR_NONE, MOE_LINEAR_RELU, MOE_LINEAR_SILU, MOE_LINEAR_GELU,
+ MOE_LINEAR_GELU_TANH) = range(5)
 
 EXPORTS = ("moe_workspace_bytes", "moe_router", "moe_dispatch", "moe_expert_ffn", "moe_combine",
            "moe_layer_forward", "moe_check_status", "moe_status_string", "moe_last_error_string",
            "moe_version", "moe_launch_count", "moe_profile_begin", "moe_profile_end",
-           "moe_dispatch_noalloc", "moe_expert_ffn_multi", "moe_workspace_layout")
+           "moe_dispatch_noalloc", "moe_expert_ffn_multi", "moe_workspace_layout",
+           "moe_route_workspace_bytes", "moe_route", "moe_route_backward", "moe_combine_backward",
+           "moe_linear_workspace_bytes", "moe_linear", "moe_linear_backward")
 PROFILE_STAGES = ("router", "dispatch", "expert_up", "expert_down", "shared_expert", "combine")
 
 
@@ -49,6 +56,22 @@ class moe_workspace_regions(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in ("topk_idx", "topk_w", "counts", "offsets", "perm",
                                                "inv_row", "drop", "x_scale", "x_gemm",
                                                "total")]
+
+
+class moe_route_config(ctypes.Structure):
+    """Mirror of ``struct moe_route_config`` in include/moe.h."""
+    _fields_ = [("T", ctypes.c_int64), ("ld", ctypes.c_int64), ("N", ctypes.c_int32),
+                ("k", ctypes.c_int32), ("score", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("n_groups", ctypes.c_int32),
+                ("topk_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class moe_linear_config(ctypes.Structure):
+    """Mirror of ``struct moe_linear_config`` in include/moe.h."""
+    _fields_ = [("M", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64),
+                ("ldr", ctypes.c_int64), ("n_in", ctypes.c_int32), ("n_out", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
 
 
 class MoeError(RuntimeError):
@@ -88,6 +111,19 @@ def lib():
         L.moe_layer_forward.argtypes = [cfgp, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P,
                                         ctypes.c_size_t, P]
         L.moe_check_status.argtypes = [P, P, ctypes.POINTER(ctypes.c_uint32)]
+        routep, linp = ctypes.POINTER(moe_route_config), ctypes.POINTER(moe_linear_config)
+        L.moe_route_workspace_bytes.argtypes = [routep]
+        L.moe_route_workspace_bytes.restype = ctypes.c_size_t
+        L.moe_route.argtypes = [routep, P, P, P, P, P, P, ctypes.c_size_t, P]
+        L.moe_route_backward.argtypes = [routep, P, P, P, P, P, P, ctypes.c_size_t, P]
+        L.moe_combine_backward.argtypes = [cfgp, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+        L.moe_linear_workspace_bytes.argtypes = [linp, ctypes.c_int32]
+        L.moe_linear_workspace_bytes.restype = ctypes.c_size_t
+        L.moe_linear.argtypes = [linp, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+        L.moe_linear_backward.argtypes = [linp, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+        for f in ("moe_route", "moe_route_backward", "moe_combine_backward", "moe_linear",
+                  "moe_linear_backward"):
+            getattr(L, f).restype = ctypes.c_int
         for f in ("moe_router", "moe_dispatch", "moe_expert_ffn", "moe_expert_ffn_multi",
                   "moe_combine", "moe_layer_forward", "moe_check_status"):
             getattr(L, f).restype = ctypes.c_int
@@ -288,3 +324,168 @@ def workspace(cfg: moe_config, device="cuda"):
     if n == 0:
         raise MoeError(MOE_ERR_INVALID_ARG, "moe_workspace_bytes")
     return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+# ------------------------------------------------------------------ the gate and the projections
+_TORCH_DTYPES = {}
+
+
+def _torch_dtype(code):
+    if not _TORCH_DTYPES:
+        import torch
+        _TORCH_DTYPES.update({MOE_F32: torch.float32, MOE_BF16: torch.bfloat16,
+                              "i32": torch.int32})
+    return _TORCH_DTYPES[code]
+
+
+def _arg(where, device, name, t, code, shape, ld=None, optional=False):
+    """Address of argument ``name`` after checking what the C call cannot see: element type,
+    shape, row stride and device.  Integers are taken as addresses, unchecked."""
+    if t is None:
+        if optional:
+            return None
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: {name} is missing")
+    if isinstance(t, int):
+        return t
+    if t.dtype is not _torch_dtype(code):
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: {name} is {t.dtype}")
+    if t.shape != shape:
+        raise MoeError(MOE_ERR_INVALID_ARG,
+                       f"{where}: {name} is {list(t.shape)}, not {list(shape)}")
+    if ld is None:
+        if not t.is_contiguous():
+            raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: {name} is not contiguous")
+    else:
+        s0, s1 = t.stride()
+        if (s1 != 1 and shape[1] > 1) or (s0 != ld and shape[0] > 1):
+            raise MoeError(MOE_ERR_INVALID_ARG,
+                           f"{where}: {name} has strides {(s0, s1)}, not {(ld, 1)}")
+    if t.device != device:
+        raise MoeError(MOE_ERR_INVALID_ARG,
+                       f"{where}: {name} is on {t.device}, the workspace on {device}")
+    return t.data_ptr()
+
+
+def _call(where, fn, workspace, stream, *args):
+    """Runs a C entry point with the workspace's device current (on ``stream``, or that
+    device's current stream)."""
+    import torch
+    dev = workspace.device
+    if dev.type != "cuda":
+        raise MoeError(MOE_ERR_WORKSPACE, f"{where}: the workspace is on {dev}")
+    nbytes = workspace.numel() * workspace.element_size()
+    if not workspace.is_contiguous():
+        raise MoeError(MOE_ERR_WORKSPACE, f"{where}: the workspace is not contiguous")
+    if dev.index == torch.cuda.current_device():
+        status = fn(*args, workspace.data_ptr(), nbytes, _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, workspace.data_ptr(), nbytes, _stream(stream))
+    if status != MOE_OK:
+        raise MoeError(status, where)
+
+
+def make_route_config(T, N, k, *, score="softmax", n_groups=0, topk_groups=0, group_top=0,
+                      renormalize=False, scale=1.0, dtype="f32", ld=0) -> moe_route_config:
+    """``ld`` = 0: rows of N logits without gaps."""
+    return moe_route_config(int(T), int(ld) or int(N), int(N), int(k),
+                            {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}[score],
+                            int(bool(renormalize)), {"f32": MOE_F32, "bf16": MOE_BF16}[dtype],
+                            int(n_groups), int(topk_groups), int(group_top), float(scale))
+
+
+def moe_route_workspace_bytes(cfg: moe_route_config) -> int:
+    return int(lib().moe_route_workspace_bytes(ctypes.byref(cfg)))
+
+
+def route_workspace(cfg: moe_route_config, device="cuda"):
+    """A zero-filled workspace tensor for ``moe_route`` and ``moe_route_backward``."""
+    return _zeros(moe_route_workspace_bytes(cfg), "moe_route_workspace_bytes", device)
+
+
+def _zeros(nbytes, where, device):
+    import torch
+    if nbytes == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, where)
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+
+
+def moe_route(cfg, logits, bias, topk_idx, topk_w, p_mean, workspace, stream=None):
+    a, dev = "moe_route", workspace.device
+    T, N, k = cfg.T, cfg.N, cfg.k
+    _call(a, lib().moe_route, workspace, stream, ctypes.byref(cfg),
+          _arg(a, dev, "logits", logits, cfg.dtype, (T, N), cfg.ld),
+          _arg(a, dev, "bias", bias, MOE_F32, (N,), optional=True),
+          _arg(a, dev, "topk_idx", topk_idx, "i32", (T, k)),
+          _arg(a, dev, "topk_w", topk_w, MOE_F32, (T, k)),
+          _arg(a, dev, "p_mean", p_mean, MOE_F32, (N,), optional=True))
+
+
+def moe_route_backward(cfg, logits, topk_idx, dtopk_w, dp_mean, dlogits, workspace, stream=None):
+    a, dev = "moe_route_backward", workspace.device
+    T, N, k = cfg.T, cfg.N, cfg.k
+    _call(a, lib().moe_route_backward, workspace, stream, ctypes.byref(cfg),
+          _arg(a, dev, "logits", logits, cfg.dtype, (T, N), cfg.ld),
+          _arg(a, dev, "topk_idx", topk_idx, "i32", (T, k), optional=dtopk_w is None),
+          _arg(a, dev, "dtopk_w", dtopk_w, MOE_F32, (T, k), optional=True),
+          _arg(a, dev, "dp_mean", dp_mean, MOE_F32, (N,), optional=True),
+          _arg(a, dev, "dlogits", dlogits, cfg.dtype, (T, N), cfg.ld))
+
+
+def moe_combine_backward(cfg, dy, y_perm, inv_row, topk_w, dy_perm, dtopk_w, workspace,
+                         stream=None):
+    a, dev = "moe_combine_backward", workspace.device
+    T, d, k = cfg.T, cfg.d, cfg.k
+    rows = T * k
+    _call(a, lib().moe_combine_backward, workspace, stream, ctypes.byref(cfg),
+          _arg(a, dev, "dy", dy, cfg.dtype, (T, d)),
+          _arg(a, dev, "y_perm", y_perm, cfg.dtype, (rows, d), optional=dtopk_w is None),
+          _arg(a, dev, "inv_row", inv_row, "i32", (rows,)),
+          _arg(a, dev, "topk_w", topk_w, MOE_F32, (T, k), optional=dy_perm is None),
+          _arg(a, dev, "dy_perm", dy_perm, cfg.dtype, (rows, d), optional=True),
+          _arg(a, dev, "dtopk_w", dtopk_w, MOE_F32, (T, k), optional=True))
+
+
+def make_linear_config(M, n_in, n_out, *, act="none", dtype="bf16", out_dtype=None, ldx=0, ldy=0,
+                       ldr=0) -> moe_linear_config:
+    """``out_dtype`` None: that of the operands; a row stride of 0: rows without gaps."""
+    types = {"f32": MOE_F32, "bf16": MOE_BF16}
+    acts = {"none": MOE_LINEAR_NONE, "relu": MOE_LINEAR_RELU, "silu": MOE_LINEAR_SILU,
+            "gelu": MOE_LINEAR_GELU, "gelu_tanh": MOE_LINEAR_GELU_TANH}
+    return moe_linear_config(int(M), int(ldx) or int(n_in), int(ldy) or int(n_out),
+                             int(ldr) or int(n_out), int(n_in), int(n_out), acts[act],
+                             types[dtype], types[out_dtype or dtype])
+
+
+def moe_linear_workspace_bytes(cfg: moe_linear_config, backward=True) -> int:
+    return int(lib().moe_linear_workspace_bytes(ctypes.byref(cfg), int(bool(backward))))
+
+
+def linear_workspace(cfg: moe_linear_config, device="cuda", backward=True):
+    """A zero-filled workspace tensor for ``moe_linear`` (and ``moe_linear_backward``)."""
+    return _zeros(moe_linear_workspace_bytes(cfg, backward), "moe_linear_workspace_bytes", device)
+
+
+def moe_linear(cfg, x, W, bias, residual, y, preact, workspace, stream=None):
+    a, dev = "moe_linear", workspace.device
+    M, K, N = cfg.M, cfg.n_in, cfg.n_out
+    _call(a, lib().moe_linear, workspace, stream, ctypes.byref(cfg),
+          _arg(a, dev, "x", x, cfg.dtype, (M, K), cfg.ldx),
+          _arg(a, dev, "W", W, cfg.dtype, (N, K)),
+          _arg(a, dev, "bias", bias, MOE_F32, (N,), optional=True),
+          _arg(a, dev, "residual", residual, cfg.out_dtype, (M, N), cfg.ldr, optional=True),
+          _arg(a, dev, "y", y, cfg.out_dtype, (M, N), cfg.ldy),
+          _arg(a, dev, "preact", preact, cfg.dtype, (M, N), optional=True))
+
+
+def moe_linear_backward(cfg, dy, x, W, preact, dx, dW, db, workspace, stream=None):
+    a, dev = "moe_linear_backward", workspace.device
+    M, K, N = cfg.M, cfg.n_in, cfg.n_out
+    _call(a, lib().moe_linear_backward, workspace, stream, ctypes.byref(cfg),
+          _arg(a, dev, "dy", dy, cfg.out_dtype, (M, N), cfg.ldy),
+          _arg(a, dev, "x", x, cfg.dtype, (M, K), cfg.ldx, optional=dW is None),
+          _arg(a, dev, "W", W, cfg.dtype, (N, K), optional=dx is None),
+          _arg(a, dev, "preact", preact, cfg.dtype, (M, N), optional=cfg.act == MOE_LINEAR_NONE),
+          _arg(a, dev, "dx", dx, cfg.dtype, (M, K), cfg.ldx, optional=True),
+          _arg(a, dev, "dW", dW, cfg.dtype, (N, K), optional=True),
+          _arg(a, dev, "db", db, MOE_F32, (N,), optional=True))

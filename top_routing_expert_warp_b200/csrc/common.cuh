@@ -14,8 +14,9 @@ namespace moe {
 // ------------------------------------------------------------------ status
 // Bits of the device status word (first 4 bytes of the workspace).
 enum : uint32_t {
-    DEV_BAD_EXPERT = 1u << 0,   // dispatch saw an expert index outside [0, N)
-    DEV_BAD_ROW = 1u << 1,      // combine saw a row index outside [0, T*k)
+    DEV_BAD_EXPERT = 1u << 0,   // dispatch or route's gradient saw an expert index outside [0, N)
+    DEV_BAD_ROW = 1u << 1,      // combine (or its gradient) saw a row index outside [0, T*k)
+    DEV_NAN_LOGIT = 1u << 2,    // route saw a NaN logit or bias
     DEV_TIMEOUT_PRODUCER = 1u << 4,
     DEV_TIMEOUT_MMA = 1u << 5,
     DEV_TIMEOUT_EPILOGUE = 1u << 6,

@@ -224,4 +224,84 @@ cudaError_t launch_combine(int dtype, const void *y_perm, const int32_t *inv_row
                            const float *topk_w, const void *y_shared, void *y, int64_t T,
                            int32_t d, int32_t k, uint32_t *status, cudaStream_t stream);
 
+// Routing of given logits and its gradient: see route.cu.
+struct RouteLaunch {
+    int dtype;
+    int score;               // MOE_SCORE_*
+    const void *logits;      // [T, ld]
+    const float *bias;       // [N] or null
+    int64_t T, ld;
+    int32_t N, k, renormalize;
+    int32_t n_groups, topk_groups, group_top;   // 0: no nodes
+    float scale;
+    int32_t *topk_idx;
+    float *topk_w;
+    float *p_mean;           // or null
+    double *p_part;          // [blocks, N] workspace
+    uint32_t *status;
+};
+constexpr int kRouteMaxBlocks = 592;
+cudaError_t launch_route(const RouteLaunch &L, cudaStream_t stream);
+struct RouteGradLaunch {
+    int dtype;
+    int score;
+    const void *logits;
+    const int32_t *topk_idx;
+    const float *dtopk_w;    // or null
+    const float *dp_mean;    // or null
+    void *dlogits;
+    int64_t T, ld;
+    int32_t N, k, renormalize;
+    float scale;
+    uint32_t *status;
+};
+cudaError_t launch_route_grad(const RouteGradLaunch &L, cudaStream_t stream);
+
+// Gradient of the combine: see combine_grad.cu.
+cudaError_t launch_combine_grad(int dtype, const void *dy, const void *y_perm,
+                                const int32_t *inv_row, const float *topk_w, void *dy_perm,
+                                float *dtopk_w, int64_t T, int32_t d, int32_t k,
+                                uint32_t *status, cudaStream_t stream);
+
+// One product of a dense projection: D[i, j] = sum_k P(i, k) Q(j, k), out =
+// act(D + bias) + residual.  P(i, k) = P[i ldp + k] when p_kmajor, else
+// P[k ldp + i]; Q likewise.  See linear_simt.cu.
+struct LinearGemm {
+    int dtype;               // of P, Q, preact
+    bool out_f32;            // out and residual are fp32 (else dtype)
+    int act;                 // MOE_LINEAR_*
+    const void *P, *Q;
+    int64_t ldp, ldq;
+    bool p_kmajor, q_kmajor;
+    int64_t I;
+    int32_t J;
+    int64_t K;
+    void *out;
+    int64_t ldo;
+    const float *bias;
+    const void *residual;
+    int64_t ldr;
+    void *preact;            // [I, J]
+    uint32_t *status;
+};
+cudaError_t launch_linear_simt(const LinearGemm &L, cudaStream_t stream);
+// dz = dy * act'(z) and its column sums.
+constexpr int kDzMaxRowBlocks = 64;
+struct LinearDz {
+    int dtype;               // of z, dz
+    bool out_f32;            // dy is fp32
+    int act;
+    const void *dy;
+    int64_t ldy;
+    const void *z;           // [M, n] or null
+    int64_t M;
+    int32_t n;
+    void *dz;                // [M, ldz] or null
+    int64_t ldz;
+    float *part;             // [row_blocks, n]
+    int32_t row_blocks;
+    float *db;               // [n] or null
+};
+cudaError_t launch_linear_dz(const LinearDz &L, cudaStream_t stream);
+
 }  // namespace moe

@@ -1,0 +1,98 @@
+// Activations of the dense projections and the element-wise end of a tile,
+// shared by the CUDA-core and the tensor-core kernels.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "moe.h"
+
+namespace moe {
+namespace lin {
+
+// act(z), fp32.  The tanh form of GELU is z times a logistic function:
+// (1 + tanh u) / 2 = 1 / (1 + e^{-2u}).
+template <int ACT>
+__device__ __forceinline__ float act_fwd(float z)
+{
+    if (ACT == MOE_LINEAR_RELU)
+        return z < 0.0f ? 0.0f : z;      // a NaN stays one
+    if (ACT == MOE_LINEAR_SILU)
+        return z / (1.0f + expf(-z));
+    if (ACT == MOE_LINEAR_GELU)
+        return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+    if (ACT == MOE_LINEAR_GELU_TANH) {
+        const float u = 0.79788456080286536f * fmaf(0.044715f * z, z * z, z);
+        return z / (1.0f + expf(-2.0f * u));
+    }
+    return z;
+}
+
+// act'(z), fp32.
+template <int ACT>
+__device__ __forceinline__ float act_bwd(float z)
+{
+    if (ACT == MOE_LINEAR_RELU)
+        return z > 0.0f ? 1.0f : 0.0f;
+    if (ACT == MOE_LINEAR_SILU) {
+        const float s = 1.0f / (1.0f + expf(-z));
+        return s * fmaf(z, 1.0f - s, 1.0f);
+    }
+    if (ACT == MOE_LINEAR_GELU)
+        return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) +
+               z * 0.39894228040143268f * expf(-0.5f * z * z);
+    if (ACT == MOE_LINEAR_GELU_TANH) {
+        const float u = 0.79788456080286536f * fmaf(0.044715f * z, z * z, z);
+        const float p = 1.0f / (1.0f + expf(-2.0f * u));
+        // beyond |z| = 20 p (1 - p) is 0 and the other factors need not overflow
+        const float zc = fminf(fmaxf(z, -20.0f), 20.0f);
+        const float du = 0.79788456080286536f * fmaf(3.0f * 0.044715f * zc, zc, 1.0f);
+        return fmaf(2.0f * zc * du, p * (1.0f - p), p);
+    }
+    return 1.0f;
+}
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void put(float *p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+// act(z + bias) + residual for one element; writes z to preact if wanted.
+struct Epilogue {
+    void *out;               // [rows, ldo]
+    int64_t ldo;
+    const float *bias;       // [cols] or null
+    const void *residual;    // [rows, ldr] of the output type, or null
+    int64_t ldr;
+    void *preact;            // [rows, cols] of the operand type, or null
+    int32_t rows, cols;
+};
+
+template <int ACT, typename TO, typename TP>
+__device__ __forceinline__ void finish(const Epilogue &ep, int64_t row, int col, float z)
+{
+    if (ep.bias)
+        z += ep.bias[col];
+    if (ep.preact)
+        put(static_cast<TP *>(ep.preact) + row * ep.cols + col, z);
+    float y = act_fwd<ACT>(z);
+    if (ep.residual)
+        y += to_f32(static_cast<const TO *>(ep.residual)[row * ep.ldr + col]);
+    put(static_cast<TO *>(ep.out) + row * ep.ldo + col, y);
+}
+
+// Calls f with the activation as a constant.
+template <typename F>
+void with_act(int act, F f)
+{
+    switch (act) {
+    case MOE_LINEAR_RELU: f(std::integral_constant<int, MOE_LINEAR_RELU>()); break;
+    case MOE_LINEAR_SILU: f(std::integral_constant<int, MOE_LINEAR_SILU>()); break;
+    case MOE_LINEAR_GELU: f(std::integral_constant<int, MOE_LINEAR_GELU>()); break;
+    case MOE_LINEAR_GELU_TANH: f(std::integral_constant<int, MOE_LINEAR_GELU_TANH>()); break;
+    default: f(std::integral_constant<int, MOE_LINEAR_NONE>()); break;
+    }
+}
+
+}  // namespace lin
+}  // namespace moe

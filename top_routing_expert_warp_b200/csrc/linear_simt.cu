@@ -1,0 +1,193 @@
+// Dense products on the CUDA cores, for fp32 operands (TF32 would not meet an
+// fp32 bound), with the projection's epilogue, and the element-wise half of
+// the projection's gradient.
+//
+//   D[i, j] = sum_k P(i, k) Q(j, k);  out = act(D + bias) + residual
+//
+// The three products of a projection differ in which index of an operand is
+// contiguous:
+//   y  = x W^T      P = x  (k contiguous),      Q = W (k contiguous)
+//   dx = dz W       P = dz (k contiguous),      Q = W^T (j contiguous)
+//   dW = dz^T x     P = dz^T (i contiguous),    Q = x^T (j contiguous)
+#include <type_traits>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "linear.cuh"
+#include "moe.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int TM = 64, TN = 64, TK = 16;
+
+// One 64 x 64 tile per block, 4 x 4 outputs per thread.
+template <typename T, typename TO, int ACT, bool P_K, bool Q_K>
+__global__ void __launch_bounds__(kThreads)
+    linear_simt_kernel(const T *__restrict__ P, int64_t ldp, const T *__restrict__ Q, int64_t ldq,
+                       int64_t I, int J, int64_t K, lin::Epilogue ep)
+{
+    grid_dep_wait();
+    __shared__ float s_p[TK][TM + 4], s_q[TK][TN + 4];
+    const int tid = threadIdx.x;
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * TM;
+    const int64_t j0 = static_cast<int64_t>(blockIdx.y) * TN;
+    const int ti = (tid >> 4) * 4, tj = (tid & 15) * 4;
+    float acc[4][4] = {};
+    for (int64_t k0 = 0; k0 < K; k0 += TK) {
+        for (int e = tid; e < TM * TK; e += kThreads) {
+            const int i = P_K ? e / TK : e % TM, k = P_K ? e % TK : e / TM;
+            float v = 0.0f;
+            if (i0 + i < I && k0 + k < K)
+                v = lin::to_f32(P_K ? P[(i0 + i) * ldp + k0 + k] : P[(k0 + k) * ldp + i0 + i]);
+            s_p[k][i] = v;
+        }
+        for (int e = tid; e < TN * TK; e += kThreads) {
+            const int j = Q_K ? e / TK : e % TN, k = Q_K ? e % TK : e / TN;
+            float v = 0.0f;
+            if (j0 + j < J && k0 + k < K)
+                v = lin::to_f32(Q_K ? Q[(j0 + j) * ldq + k0 + k] : Q[(k0 + k) * ldq + j0 + j]);
+            s_q[k][j] = v;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < TK; ++k) {
+            float a[4], b[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                a[x] = s_p[k][ti + x];
+                b[x] = s_q[k][tj + x];
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    acc[x][y] = fmaf(a[x], b[y], acc[x][y]);
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+            if (i0 + ti + x < I && j0 + tj + y < J)
+                lin::finish<ACT, TO, T>(ep, i0 + ti + x, static_cast<int>(j0) + tj + y, acc[x][y]);
+}
+
+// dz = dy * act'(z) in the operand type, and this row block's column sums of
+// the unrounded dz.  One thread per column, rows in order.
+template <typename T, typename TO, int ACT>
+__global__ void __launch_bounds__(kThreads)
+    linear_dz_kernel(const TO *__restrict__ dy, int64_t ldy, const T *__restrict__ z, int64_t M,
+                     int n, T *__restrict__ dz, int64_t ldz, float *__restrict__ part,
+                     int64_t rows_per_block)
+{
+    grid_dep_wait();
+    const int col = blockIdx.x * kThreads + threadIdx.x;
+    if (col >= n)
+        return;
+    const int64_t r0 = blockIdx.y * rows_per_block;
+    const int64_t r1 = r0 + rows_per_block < M ? r0 + rows_per_block : M;
+    float sum = 0.0f;
+    for (int64_t r = r0; r < r1; ++r) {
+        float g = lin::to_f32(dy[r * ldy + col]);
+        if (ACT != MOE_LINEAR_NONE)
+            g *= lin::act_bwd<ACT>(lin::to_f32(z[r * n + col]));
+        sum += g;
+        if (dz)
+            lin::put(dz + r * ldz + col, g);
+    }
+    if (part)
+        part[static_cast<int64_t>(blockIdx.y) * n + col] = sum;
+}
+
+__global__ void __launch_bounds__(kThreads)
+    linear_db_kernel(const float *__restrict__ part, int blocks, int n, float *__restrict__ db)
+{
+    grid_dep_wait();
+    const int col = blockIdx.x * kThreads + threadIdx.x;
+    if (col >= n)
+        return;
+    float sum = 0.0f;
+    for (int b = 0; b < blocks; ++b)
+        sum += part[static_cast<int64_t>(b) * n + col];
+    db[col] = sum;
+}
+
+template <typename T, typename TO>
+void run_simt(const LinearGemm &L, cudaStream_t stream)
+{
+    const dim3 grid(static_cast<unsigned>((L.I + TM - 1) / TM),
+                    static_cast<unsigned>((L.J + TN - 1) / TN), 1);
+    const T *P = static_cast<const T *>(L.P);
+    const T *Q = static_cast<const T *>(L.Q);
+    lin::Epilogue ep;
+    ep.out = L.out;
+    ep.ldo = L.ldo;
+    ep.bias = L.bias;
+    ep.residual = L.residual;
+    ep.ldr = L.ldr;
+    ep.preact = L.preact;
+    ep.rows = static_cast<int32_t>(L.I);
+    ep.cols = L.J;
+    if (L.p_kmajor && L.q_kmajor)
+        lin::with_act(L.act, [&](auto a) {
+            launch_k(linear_simt_kernel<T, TO, decltype(a)::value, true, true>, grid, kThreads, 0,
+                     stream, P, L.ldp, Q, L.ldq, L.I, L.J, L.K, ep);
+        });
+    else if (L.p_kmajor)
+        launch_k(linear_simt_kernel<T, TO, MOE_LINEAR_NONE, true, false>, grid, kThreads, 0,
+                 stream, P, L.ldp, Q, L.ldq, L.I, L.J, L.K, ep);
+    else
+        launch_k(linear_simt_kernel<T, TO, MOE_LINEAR_NONE, false, false>, grid, kThreads, 0,
+                 stream, P, L.ldp, Q, L.ldq, L.I, L.J, L.K, ep);
+    count_launches(1);
+}
+
+template <typename T, typename TO>
+void run_dz(const LinearDz &L, cudaStream_t stream)
+{
+    const int64_t per = (L.M + L.row_blocks - 1) / L.row_blocks;
+    const dim3 grid(static_cast<unsigned>((L.n + kThreads - 1) / kThreads),
+                    static_cast<unsigned>(L.row_blocks), 1);
+    lin::with_act(L.act, [&](auto a) {
+        launch_k(linear_dz_kernel<T, TO, decltype(a)::value>, grid, kThreads, 0, stream,
+                 static_cast<const TO *>(L.dy), L.ldy, static_cast<const T *>(L.z), L.M, L.n,
+                 static_cast<T *>(L.dz), L.ldz, L.db ? L.part : nullptr, per);
+    });
+    count_launches(1);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_simt(const LinearGemm &L, cudaStream_t stream)
+{
+    if (L.dtype == MOE_F32)
+        run_simt<float, float>(L, stream);
+    else if (L.out_f32)
+        run_simt<__nv_bfloat16, float>(L, stream);
+    else
+        run_simt<__nv_bfloat16, __nv_bfloat16>(L, stream);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_linear_dz(const LinearDz &L, cudaStream_t stream)
+{
+    if (L.dtype == MOE_F32)
+        run_dz<float, float>(L, stream);
+    else if (L.out_f32)
+        run_dz<__nv_bfloat16, float>(L, stream);
+    else
+        run_dz<__nv_bfloat16, __nv_bfloat16>(L, stream);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !L.db)
+        return e;
+    launch_k(linear_db_kernel, dim3((L.n + kThreads - 1) / kThreads), kThreads, 0, stream,
+             static_cast<const float *>(L.part), L.row_blocks, L.n, L.db);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+}  // namespace moe

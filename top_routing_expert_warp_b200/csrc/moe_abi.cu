@@ -1,6 +1,7 @@
 // C ABI of libmoe_b200 (declared in include/moe.h): argument validation,
 // workspace layout and the launch sequence of each stage.  No kernel code.
 #include <atomic>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
@@ -403,6 +404,95 @@ moe_status run_ffn(const moe_config &c, const void *A, const float *row_scale, i
     return MOE_OK;
 }
 
+// ---------------------------------------------------------------- the gate
+bool route_config_ok(const moe_route_config *c)
+{
+    if (!c)
+        return false;
+    if (c->T < 0 || c->N < 1 || c->N > 256 || c->k < 1 || c->k > 8 || c->k > c->N || c->ld < c->N)
+        return false;
+    if (c->T > 0x7FFFFFFFll / c->k || c->ld > (1ll << 40))
+        return false;
+    if (c->dtype != MOE_F32 && c->dtype != MOE_BF16)
+        return false;
+    if (c->score != MOE_SCORE_SOFTMAX && c->score != MOE_SCORE_SIGMOID)
+        return false;
+    if (c->renormalize != 0 && c->renormalize != 1)
+        return false;
+    if (!std::isfinite(c->scale))
+        return false;
+    if (c->n_groups < 0 || c->topk_groups < 0 || c->group_top < 0)
+        return false;
+    if (c->n_groups > 1 && c->topk_groups < c->n_groups) {
+        if (c->n_groups > 32 || c->N % c->n_groups != 0 || c->topk_groups < 1 ||
+            c->k > c->topk_groups * (c->N / c->n_groups) || c->group_top < 1 ||
+            c->group_top > c->N / c->n_groups)
+            return false;
+    }
+    return true;
+}
+
+// Status word, then the blocks' sums of the scores.
+constexpr size_t kRoutePart = 256;
+size_t route_workspace(const moe_route_config &c)
+{
+    return kRoutePart + up256(static_cast<size_t>(moe::kRouteMaxBlocks) * c.N * sizeof(double));
+}
+
+// A workspace that starts with the status word and has `need` bytes.
+moe_status check_plain_ws(void *ws, size_t ws_bytes, size_t need)
+{
+    return (!ws || !aligned(ws, 256) || ws_bytes < need) ? MOE_ERR_WORKSPACE : MOE_OK;
+}
+
+// ---------------------------------------------------------------- projections
+bool linear_config_ok(const moe_linear_config *c)
+{
+    if (!c)
+        return false;
+    if (c->M < 0 || c->M > 0x7FFFFFFFll || c->n_in < 1 || c->n_out < 1 || c->n_in > (1 << 20) ||
+        c->n_out > (1 << 20))
+        return false;
+    if (c->dtype != MOE_F32 && c->dtype != MOE_BF16)
+        return false;
+    if (c->out_dtype != c->dtype && c->out_dtype != MOE_F32)
+        return false;
+    if (c->act < MOE_LINEAR_NONE || c->act > MOE_LINEAR_GELU_TANH)
+        return false;
+    const int align = c->dtype == MOE_BF16 ? 8 : 4;
+    if (c->n_in % align || c->ldx % align)
+        return false;
+    if (c->ldx < c->n_in || c->ldy < c->n_out || c->ldr < c->n_out)
+        return false;
+    const int64_t top = 1ll << 32;      // strides: M * ld stays far inside 64 bits
+    return c->ldx <= top && c->ldy <= top && c->ldr <= top;
+}
+
+struct LinearLayout {
+    size_t status, db_part, dz, total;
+    int64_t ldz;
+};
+
+LinearLayout linear_layout(const moe_linear_config &c, bool backward)
+{
+    LinearLayout L{};
+    size_t o = 0;
+    auto take = [&](size_t bytes) {
+        size_t at = o;
+        o += up256(bytes);
+        return at;
+    };
+    const int64_t es = elem_size(c.dtype);
+    L.ldz = (c.n_out + 7) / 8 * 8;
+    L.status = take(256);
+    if (backward) {
+        L.db_part = take(static_cast<size_t>(moe::kDzMaxRowBlocks) * c.n_out * sizeof(float));
+        L.dz = take(static_cast<size_t>(c.M) * L.ldz * es);
+    }
+    L.total = o;
+    return L;
+}
+
 }  // namespace
 
 extern "C" {
@@ -700,6 +790,236 @@ moe_status moe_layer_forward(const moe_config *cfg, const void *x, const void *W
     prof_mark(6, s);
     if (g_prof.on && g_prof.steps < g_prof.max_steps)
         ++g_prof.steps;
+    return MOE_OK;
+}
+
+size_t moe_route_workspace_bytes(const moe_route_config *cfg)
+{
+    return route_config_ok(cfg) ? route_workspace(*cfg) : 0;
+}
+
+moe_status moe_route(const moe_route_config *cfg, const void *logits, const float *bias,
+                     int32_t *topk_idx, float *topk_w, float *p_mean,
+                     void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!route_config_ok(cfg))
+        return MOE_ERR_INVALID_ARG;
+    const moe_route_config &c = *cfg;
+    if (c.T > 0 && (!logits || !topk_idx || !topk_w || !aligned(logits, elem_size(c.dtype))))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(bias, 4) || !aligned(topk_idx, 4) || !aligned(topk_w, 4) || !aligned(p_mean, 4))
+        return MOE_ERR_INVALID_ARG;
+    const moe_status st = check_plain_ws(workspace, workspace_bytes, route_workspace(c));
+    if (st != MOE_OK)
+        return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (c.T == 0) {
+        if (p_mean)
+            MOE_CUDA(cudaMemsetAsync(p_mean, 0, c.N * sizeof(float), s));
+        return MOE_OK;
+    }
+    const bool nodes = c.n_groups > 1 && c.topk_groups < c.n_groups;
+    moe::RouteLaunch R{};
+    R.dtype = c.dtype;
+    R.score = c.score;
+    R.logits = logits;
+    R.bias = bias;
+    R.T = c.T;
+    R.ld = c.ld;
+    R.N = c.N;
+    R.k = c.k;
+    R.renormalize = c.renormalize;
+    R.n_groups = nodes ? c.n_groups : 0;
+    R.topk_groups = nodes ? c.topk_groups : 0;
+    R.group_top = nodes ? c.group_top : 0;
+    R.scale = c.scale;
+    R.topk_idx = topk_idx;
+    R.topk_w = topk_w;
+    R.p_mean = p_mean;
+    R.p_part = reinterpret_cast<double *>(static_cast<uint8_t *>(workspace) + kRoutePart);
+    R.status = static_cast<uint32_t *>(workspace);
+    MOE_CUDA(moe::launch_route(R, s));
+    return MOE_OK;
+}
+
+moe_status moe_route_backward(const moe_route_config *cfg, const void *logits,
+                              const int32_t *topk_idx, const float *dtopk_w,
+                              const float *dp_mean, void *dlogits,
+                              void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!route_config_ok(cfg))
+        return MOE_ERR_INVALID_ARG;
+    const moe_route_config &c = *cfg;
+    if (c.T > 0 && (!logits || !dlogits || (dtopk_w && !topk_idx) ||
+                    !aligned(logits, elem_size(c.dtype)) || !aligned(dlogits, elem_size(c.dtype))))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(topk_idx, 4) || !aligned(dtopk_w, 4) || !aligned(dp_mean, 4))
+        return MOE_ERR_INVALID_ARG;
+    const moe_status st = check_plain_ws(workspace, workspace_bytes, route_workspace(c));
+    if (st != MOE_OK)
+        return st;
+    if (c.T == 0)
+        return MOE_OK;
+    moe::RouteGradLaunch R{};
+    R.dtype = c.dtype;
+    R.score = c.score;
+    R.logits = logits;
+    R.topk_idx = topk_idx;
+    R.dtopk_w = dtopk_w;
+    R.dp_mean = dp_mean;
+    R.dlogits = dlogits;
+    R.T = c.T;
+    R.ld = c.ld;
+    R.N = c.N;
+    R.k = c.k;
+    R.renormalize = c.renormalize;
+    R.scale = c.scale;
+    R.status = static_cast<uint32_t *>(workspace);
+    MOE_CUDA(moe::launch_route_grad(R, static_cast<cudaStream_t>(stream)));
+    return MOE_OK;
+}
+
+moe_status moe_combine_backward(const moe_config *cfg, const void *dy, const void *y_perm,
+                                const int32_t *inv_row, const float *topk_w, void *dy_perm,
+                                float *dtopk_w, void *workspace, size_t workspace_bytes,
+                                void *stream)
+{
+    if (!config_ok(cfg))
+        return MOE_ERR_INVALID_ARG;
+    if (cfg->T > 0 && ((!dy_perm && !dtopk_w) || !dy || !inv_row || (dtopk_w && !y_perm) || (dy_perm && !topk_w)))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(dy, 16) || !aligned(y_perm, 16) || !aligned(dy_perm, 16) || !aligned(inv_row, 4) ||
+        !aligned(topk_w, 4) || !aligned(dtopk_w, 4))
+        return MOE_ERR_INVALID_ARG;
+    Ws w;
+    const moe_status st = check_ws(cfg, workspace, workspace_bytes, &w);
+    if (st != MOE_OK)
+        return st;
+    MOE_CUDA(moe::launch_combine_grad(cfg->dtype, dy, y_perm, inv_row, topk_w, dy_perm, dtopk_w,
+                                      cfg->T, cfg->d, cfg->k, w.status(),
+                                      static_cast<cudaStream_t>(stream)));
+    return MOE_OK;
+}
+
+size_t moe_linear_workspace_bytes(const moe_linear_config *cfg, int32_t backward)
+{
+    return linear_config_ok(cfg) ? linear_layout(*cfg, backward != 0).total : 0;
+}
+
+moe_status moe_linear(const moe_linear_config *cfg, const void *x, const void *W,
+                      const float *bias, const void *residual, void *y, void *preact,
+                      void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!linear_config_ok(cfg))
+        return MOE_ERR_INVALID_ARG;
+    const moe_linear_config &c = *cfg;
+    const int os = elem_size(c.out_dtype);
+    if (c.M > 0 && (!x || !W || !y))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(W, 16) || !aligned(bias, 4) || !aligned(residual, os) ||
+        !aligned(y, os) || !aligned(preact, elem_size(c.dtype)))
+        return MOE_ERR_INVALID_ARG;
+    const LinearLayout L = linear_layout(c, false);
+    const moe_status st = check_plain_ws(workspace, workspace_bytes, L.total);
+    if (st != MOE_OK)
+        return st;
+    if (c.M == 0)
+        return MOE_OK;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    moe::LinearGemm G{};
+    G.dtype = c.dtype;
+    G.out_f32 = c.out_dtype == MOE_F32;
+    G.act = c.act;
+    G.P = x;
+    G.ldp = c.ldx;
+    G.p_kmajor = true;
+    G.Q = W;
+    G.ldq = c.n_in;
+    G.q_kmajor = true;
+    G.I = c.M;
+    G.J = c.n_out;
+    G.K = c.n_in;
+    G.out = y;
+    G.ldo = c.ldy;
+    G.bias = bias;
+    G.residual = residual;
+    G.ldr = c.ldr;
+    G.preact = preact;
+    G.status = reinterpret_cast<uint32_t *>(ws + L.status);
+    MOE_CUDA(moe::launch_linear_simt(G, static_cast<cudaStream_t>(stream)));
+    return MOE_OK;
+}
+
+moe_status moe_linear_backward(const moe_linear_config *cfg, const void *dy, const void *x,
+                               const void *W, const void *preact, void *dx, void *dW, float *db,
+                               void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!linear_config_ok(cfg))
+        return MOE_ERR_INVALID_ARG;
+    const moe_linear_config &c = *cfg;
+    const int es = elem_size(c.dtype), os = elem_size(c.out_dtype);
+    const bool act = c.act != MOE_LINEAR_NONE;
+    if (c.M > 0 && ((!dx && !dW && !db) || !dy || (dW && !x) || (dx && !W) || (act && !preact)))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(dy, os) || !aligned(x, 16) || !aligned(W, 16) || !aligned(preact, es) ||
+        !aligned(dx, 16) || !aligned(dW, 16) || !aligned(db, 4))
+        return MOE_ERR_INVALID_ARG;
+    const LinearLayout L = linear_layout(c, true);
+    const moe_status st = check_plain_ws(workspace, workspace_bytes, L.total);
+    if (st != MOE_OK)
+        return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (c.M == 0) {
+        if (dW)
+            MOE_CUDA(cudaMemsetAsync(dW, 0, static_cast<size_t>(c.n_out) * c.n_in * es, s));
+        if (db)
+            MOE_CUDA(cudaMemsetAsync(db, 0, c.n_out * sizeof(float), s));
+        return MOE_OK;
+    }
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    moe::LinearDz Z{};
+    Z.dtype = c.dtype;
+    Z.out_f32 = c.out_dtype == MOE_F32;
+    Z.act = c.act;
+    Z.dy = dy;
+    Z.ldy = c.ldy;
+    Z.z = preact;
+    Z.M = c.M;
+    Z.n = c.n_out;
+    Z.dz = (dx || dW) ? ws + L.dz : nullptr;
+    Z.ldz = L.ldz;
+    Z.part = reinterpret_cast<float *>(ws + L.db_part);
+    Z.row_blocks = static_cast<int32_t>(c.M < moe::kDzMaxRowBlocks ? c.M : moe::kDzMaxRowBlocks);
+    Z.db = db;
+    MOE_CUDA(moe::launch_linear_dz(Z, s));
+    moe::LinearGemm G{};
+    G.dtype = c.dtype;
+    G.act = MOE_LINEAR_NONE;
+    G.P = Z.dz;
+    G.ldp = L.ldz;
+    G.q_kmajor = false;
+    G.J = c.n_in;
+    G.status = reinterpret_cast<uint32_t *>(ws + L.status);
+    if (dx) {
+        G.p_kmajor = true;
+        G.Q = W;
+        G.ldq = c.n_in;
+        G.I = c.M;
+        G.K = c.n_out;
+        G.out = dx;
+        G.ldo = c.ldx;
+        MOE_CUDA(moe::launch_linear_simt(G, s));
+    }
+    if (dW) {
+        G.p_kmajor = false;
+        G.Q = x;
+        G.ldq = c.ldx;
+        G.I = c.n_out;
+        G.K = c.M;
+        G.out = dW;
+        G.ldo = c.n_in;
+        MOE_CUDA(moe::launch_linear_simt(G, s));
+    }
     return MOE_OK;
 }
 
