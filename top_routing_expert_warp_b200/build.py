@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libmoe_b200.so")
 
 SOURCES = ["moe_abi.cu", "gemm_tc.cu", "gemm_tc2t.cu", "router.cu", "dispatch.cu", "combine.cu",
            "ffn_simt.cu", "dispatch_noalloc.cu", "gemm_tc2.cu", "layer_small.cu",
-           "route.cu", "combine_grad.cu", "linear_simt.cu"]
+           "route.cu", "combine_grad.cu", "linear_simt.cu", "linear_tc.cu"]
 HEADERS = ["common.cuh", "kernels.h", "router_small.cuh", "linear.cuh"]
 
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",

@@ -282,8 +282,23 @@ struct LinearGemm {
     const void *residual;
     int64_t ldr;
     void *preact;            // [I, J]
+    float *part;             // partial tiles, linear_plan_part_bytes (bf16 operands)
+    uint32_t *tickets;       // kLinearMaxTickets words, zero between launches
     uint32_t *status;
 };
+// bf16 operands on the tensor cores: see linear_tc.cu.  The plan, and with it
+// the workspace, depends on the sizes alone.
+struct LinearPlan {
+    int cg;                  // CTAs per tile
+    bool swap;               // the transposed product
+    int bn;                  // tile columns
+    int splits;              // slices of k per tile
+    int64_t tiles;
+};
+constexpr int kLinearMaxTickets = 256;
+LinearPlan linear_plan(int64_t I, int64_t J, int64_t K, bool may_swap);
+size_t linear_plan_part_bytes(const LinearPlan &pl);
+cudaError_t launch_linear_tc(const LinearGemm &L, cudaStream_t stream);
 cudaError_t launch_linear_simt(const LinearGemm &L, cudaStream_t stream);
 // dz = dy * act'(z) and its column sums.
 constexpr int kDzMaxRowBlocks = 64;

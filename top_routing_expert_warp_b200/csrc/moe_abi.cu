@@ -1,5 +1,6 @@
 // C ABI of libmoe_b200 (declared in include/moe.h): argument validation,
 // workspace layout and the launch sequence of each stage.  No kernel code.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdio>
@@ -469,7 +470,7 @@ bool linear_config_ok(const moe_linear_config *c)
 }
 
 struct LinearLayout {
-    size_t status, db_part, dz, total;
+    size_t status, tickets, part, db_part, dz, total;
     int64_t ldz;
 };
 
@@ -485,12 +486,36 @@ LinearLayout linear_layout(const moe_linear_config &c, bool backward)
     const int64_t es = elem_size(c.dtype);
     L.ldz = (c.n_out + 7) / 8 * 8;
     L.status = take(256);
+    if (c.dtype == MOE_BF16 && c.M > 0) {
+        L.tickets = take(moe::kLinearMaxTickets * sizeof(uint32_t));
+        auto part = [](int64_t I, int64_t J, int64_t K, bool swap) {
+            return moe::linear_plan_part_bytes(moe::linear_plan(I, J, K, swap));
+        };
+        size_t most = part(c.M, c.n_out, c.n_in, true);
+        if (backward) {
+            most = std::max(most, part(c.M, c.n_in, c.n_out, true));
+            most = std::max(most, part(c.n_out, c.n_in, c.M, false));
+        }
+        L.part = take(most);
+    }
     if (backward) {
         L.db_part = take(static_cast<size_t>(moe::kDzMaxRowBlocks) * c.n_out * sizeof(float));
         L.dz = take(static_cast<size_t>(c.M) * L.ldz * es);
     }
     L.total = o;
     return L;
+}
+
+void linear_scratch(moe::LinearGemm *G, uint8_t *ws, const LinearLayout &L)
+{
+    G->status = reinterpret_cast<uint32_t *>(ws + L.status);
+    G->tickets = reinterpret_cast<uint32_t *>(ws + L.tickets);
+    G->part = reinterpret_cast<float *>(ws + L.part);
+}
+
+cudaError_t launch_linear(const moe::LinearGemm &G, cudaStream_t s)
+{
+    return G.dtype == MOE_BF16 ? moe::launch_linear_tc(G, s) : moe::launch_linear_simt(G, s);
 }
 
 }  // namespace
@@ -945,8 +970,8 @@ moe_status moe_linear(const moe_linear_config *cfg, const void *x, const void *W
     G.residual = residual;
     G.ldr = c.ldr;
     G.preact = preact;
-    G.status = reinterpret_cast<uint32_t *>(ws + L.status);
-    MOE_CUDA(moe::launch_linear_simt(G, static_cast<cudaStream_t>(stream)));
+    linear_scratch(&G, ws, L);
+    MOE_CUDA(launch_linear(G, static_cast<cudaStream_t>(stream)));
     return MOE_OK;
 }
 
@@ -999,7 +1024,7 @@ moe_status moe_linear_backward(const moe_linear_config *cfg, const void *dy, con
     G.ldp = L.ldz;
     G.q_kmajor = false;
     G.J = c.n_in;
-    G.status = reinterpret_cast<uint32_t *>(ws + L.status);
+    linear_scratch(&G, ws, L);
     if (dx) {
         G.p_kmajor = true;
         G.Q = W;
@@ -1008,7 +1033,7 @@ moe_status moe_linear_backward(const moe_linear_config *cfg, const void *dy, con
         G.K = c.n_out;
         G.out = dx;
         G.ldo = c.ldx;
-        MOE_CUDA(moe::launch_linear_simt(G, s));
+        MOE_CUDA(launch_linear(G, s));
     }
     if (dW) {
         G.p_kmajor = false;
@@ -1018,7 +1043,7 @@ moe_status moe_linear_backward(const moe_linear_config *cfg, const void *dy, con
         G.K = c.M;
         G.out = dW;
         G.ldo = c.n_in;
-        MOE_CUDA(moe::launch_linear_simt(G, s));
+        MOE_CUDA(launch_linear(G, s));
     }
     return MOE_OK;
 }
