@@ -11,7 +11,6 @@
 //   e_1 .. e_k = the k largest v (of the chosen nodes), ties to the lower index
 //   w_j = scale * s_{e_j} (/ sum_j s_{e_j});   p_e = mean_t s_e / sum_e s_e
 //
-// One warp per token, VPL consecutive experts per lane.
 #include <cfloat>
 #include <cmath>
 
@@ -26,23 +25,28 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr unsigned kAll = 0xffffffffu;
-// Below this logit the logistic function is e^l to the last bit and its value
-// (or a ratio's) may underflow: ratios are formed from e^{l - max} there.
-constexpr float kTinyScore = -600.0f;
+// Below this logit the logistic function is e^l to the last bit in 32 bits and
+// its value may underflow: ratios are formed from e^{l - max} there.
+constexpr float kTinyScore = -60.0f;
 
 struct RouteParams {
     const void *logits;
     const float *bias;
     int64_t T, ld;
     int32_t N, k, softmax, renorm, n_groups, topk_groups, group_top;
+    int32_t vec;             // rows start on a lane's vector boundary
+    int32_t node_lanes;      // lanes that hold a node's values
+    int32_t node_direct;     // 1: in the order they are loaded in (else regathered)
     float scale;
     int32_t *topk_idx;
     float *topk_w;
     double *p_part;   // [gridDim.x, N] or null
+    float *p_mean;    // written by a launch of one block, or null
     uint32_t *status;
 };
 
-__device__ __forceinline__ double warp_sum(double v)
+template <typename T>
+__device__ __forceinline__ T warp_sum(T v)
 {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
@@ -50,28 +54,40 @@ __device__ __forceinline__ double warp_sum(double v)
     return v;
 }
 
-__device__ __forceinline__ float warp_sum(float v)
+// Over lanes 0-7 (the slots); the other lanes get sums of their own.
+__device__ __forceinline__ float slot_sum(float v)
 {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
+    for (int o = 4; o > 0; o >>= 1)
         v += __shfl_xor_sync(kAll, v, o);
     return v;
 }
 
-__device__ __forceinline__ float warp_max(float v)
+__device__ __forceinline__ float slot_max(float v)
 {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
+    for (int o = 4; o > 0; o >>= 1)
         v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
     return v;
 }
 
-// Bits that order as the values do (no NaN), all above 1: key 0 marks what
-// cannot be chosen, key 1 an expert that is switched off.
+// Bits that order as the values do (no NaN; -0 as +0), all above 1: key 0
+// marks what cannot be chosen, key 1 an expert that is switched off.
 __device__ __forceinline__ uint64_t order_key(double v)
 {
-    const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v + 0.0));   // -0 as +0
+    const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v + 0.0));
     return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
+}
+
+__device__ __forceinline__ uint32_t order_key(float v)
+{
+    const uint32_t b = __float_as_uint(v + 0.0f);
+    return (b >> 31) ? ~b : (b | 0x80000000u);
+}
+
+__device__ __forceinline__ float key_value(uint32_t k)
+{
+    return __uint_as_float((k >> 31) ? (k & 0x7FFFFFFFu) : ~k);
 }
 
 __device__ __forceinline__ uint64_t warp_key_max(uint64_t v)
@@ -80,6 +96,11 @@ __device__ __forceinline__ uint64_t warp_key_max(uint64_t v)
     const uint32_t lo =
         __reduce_max_sync(kAll, static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
     return (static_cast<uint64_t>(hi) << 32) | lo;
+}
+
+__device__ __forceinline__ float warp_max(float v)
+{
+    return key_value(__reduce_max_sync(kAll, order_key(v)));
 }
 
 // The logit as it counts: NaN as -inf (reported), +inf as the largest finite.
@@ -100,20 +121,226 @@ __device__ __forceinline__ float load_logit(const void *row, int e)
     return static_cast<const float *>(row)[e];
 }
 
+// A lane's VPL logits from e0 on, -inf behind the last expert.  vec: the row's
+// first element lies on a boundary of VPL elements (at most 16 bytes).
 template <int VPL, bool BF16>
-__global__ void __launch_bounds__(kThreads) route_kernel(RouteParams p)
+__device__ __forceinline__ void load_logits(const void *row, int e0, int N, bool vec,
+                                            float (&l)[VPL])
+{
+    constexpr int bytes = VPL * (BF16 ? 2 : 4);
+    const uint8_t *at = static_cast<const uint8_t *>(row) + static_cast<int64_t>(e0) * (BF16 ? 2 : 4);
+    if (VPL >= 4 && vec && e0 + VPL <= N) {
+        uint32_t w[bytes >= 8 ? bytes / 4 : 2];
+        if (bytes >= 16) {
+#pragma unroll
+            for (int i = 0; i < bytes / 16; ++i) {
+                const uint4 v = reinterpret_cast<const uint4 *>(at)[i];
+                w[4 * i] = v.x;
+                w[4 * i + 1] = v.y;
+                w[4 * i + 2] = v.z;
+                w[4 * i + 3] = v.w;
+            }
+        } else {
+            const uint2 v = *reinterpret_cast<const uint2 *>(at);
+            w[0] = v.x;
+            w[1] = v.y;
+        }
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            l[i] = BF16 ? __uint_as_float((i & 1) ? (w[i / 2] & 0xFFFF0000u) : (w[i / 2] << 16))
+                        : __uint_as_float(w[BF16 ? 0 : i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            l[i] = e0 + i < N ? load_logit<BF16>(row, e0 + i) : -INFINITY;
+    }
+}
+
+// The choice in 64 bits, from the logits: the index of lane j's slot (lanes
+// below k).  Taken for tokens whose 32-bit values are too near one another
+// (route_kernel), and for nodes of more than 4 summed values.  s_val: 256
+// doubles of this warp.
+template <int VPL, bool BF16>
+__device__ __noinline__ int choose_exact(const RouteParams &p, const void *row, double *s_val)
+{
+    const int lane = threadIdx.x & 31;
+    const int N = p.N;
+    const int e0 = lane * VPL;
+    const bool nodes = p.n_groups > 1;
+    bool ignore = false;
+    float l[VPL], mx = -INFINITY;
+    load_logits<VPL, BF16>(row, e0, N, p.vec, l);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        l[i] = clean_logit(l[i], ignore);
+        mx = fmaxf(mx, l[i]);
+    }
+    mx = warp_max(mx);
+    double s[VPL], z = 0.0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const double li = l[i];
+        if (l[i] == -INFINITY)
+            s[i] = 0.0;
+        else
+            s[i] = p.softmax ? exp(li - static_cast<double>(mx)) : 1.0 / (1.0 + exp(-li));
+        z += s[i];
+    }
+    z = warp_sum(z);
+    const double rz = p.softmax && z > 0.0 ? 1.0 / z : 1.0;
+    uint64_t key[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        float b = (p.bias && e0 + i < N) ? p.bias[e0 + i] : 0.0f;
+        b = isnan(b) ? -INFINITY : b;
+        const bool off = l[i] == -INFINITY || b == -INFINITY;
+        const double v = s[i] * rz + static_cast<double>(b);
+        if (nodes)
+            s_val[e0 + i] = off ? -INFINITY : v;
+        key[i] = e0 + i >= N ? 0ull
+                             : (off ? 1ull : order_key(p.bias ? v : static_cast<double>(l[i])));
+    }
+    if (nodes) {
+        // lane g sums the group_top largest values of node g, largest first
+        __syncwarp();
+        const int per = N / p.n_groups;
+        uint64_t gkey = 0;
+        if (lane < p.n_groups) {
+            double sum = 0.0, last = INFINITY;
+            int taken = 0;              // of the values equal to `last`
+            for (int r = 0; r < p.group_top; ++r) {
+                double best = -INFINITY;
+                int equal = 0;
+                for (int i = 0; i < per; ++i) {
+                    const double v = s_val[lane * per + i];
+                    if (v == last)
+                        ++equal;
+                    else if (v < last && v > best)
+                        best = v;
+                }
+                if (equal > taken) {
+                    best = last;
+                    ++taken;
+                } else {
+                    last = best;
+                    taken = 1;
+                }
+                if (best == -INFINITY)
+                    break;
+                sum += best;
+            }
+            gkey = order_key(sum);
+        }
+        uint32_t chosen = 0;
+        for (int r = 0; r < p.topk_groups; ++r) {
+            const uint64_t m = warp_key_max(gkey);
+            const int g = __ffs(__ballot_sync(kAll, gkey == m)) - 1;
+            chosen |= 1u << g;
+            if (lane == g)
+                gkey = 0;
+        }
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (e0 + i < N && !((chosen >> ((e0 + i) / per)) & 1u))
+                key[i] = 0;
+        __syncwarp();
+    }
+    int mine = 0;
+    for (int j = 0; j < p.k; ++j) {
+        uint64_t best = 0;
+        int bi = 0;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                bi = i;
+            }
+        const uint64_t m = warp_key_max(best);
+        const int src = __ffs(__ballot_sync(kAll, best == m)) - 1;
+        const int e = __shfl_sync(kAll, e0 + bi, src);
+        if (lane == src) {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if (i == bi)
+                    key[i] = 0;
+        }
+        if (lane == j)
+            mine = e;
+    }
+    return mine;
+}
+
+// Inserts v into a list of the M largest values, largest first.
+template <int M>
+__device__ __forceinline__ void list_insert(float (&a)[M], float v)
+{
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+        const float hi = fmaxf(a[i], v);
+        v = fminf(a[i], v);
+        a[i] = hi;
+    }
+}
+
+// Sum of the `m` (at most M) largest of the values of this lane's node, on
+// every lane of the node; -inf counts as nothing.  The lists of two halves of
+// a node merge entry by entry.
+template <int M, int VPL>
+__device__ __forceinline__ float node_sum(const float (&v)[VPL], const float *s_node, int count,
+                                          int lanes, int m)
+{
+    float a[M];
+#pragma unroll
+    for (int i = 0; i < M; ++i)
+        a[i] = -INFINITY;
+    if (s_node) {
+        for (int i = 0; i < count; ++i)
+            list_insert<M>(a, s_node[i * lanes]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            list_insert<M>(a, v[i]);
+    }
+    for (int o = 1; o < lanes; o <<= 1) {
+        float b[M];
+#pragma unroll
+        for (int i = 0; i < M; ++i)
+            b[i] = __shfl_xor_sync(kAll, a[i], o);
+#pragma unroll
+        for (int i = 0; i < M; ++i)
+            list_insert<M>(a, b[i]);
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < M; ++i)
+        if (i < m && a[i] != -INFINITY)
+            sum += a[i];
+    return sum;
+}
+
+// One warp per token, VPL consecutive experts per lane.  What bounds it is the
+// warps' issue rate (k rounds of a warp maximum, the exponentials), not the
+// bytes; so values are formed and compared in 32 bits, and a token whose
+// decisions hang on differences near the 32-bit error is decided again in
+// 64 (choose_exact).  Without a bias and nodes the 32-bit keys are the logits
+// themselves and decide exactly.
+template <int VPL, bool BF16>
+__global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__ RouteParams p)
 {
     grid_dep_wait();
-    __shared__ double s_val[kWarps][32 * VPL];
+    __shared__ double s_val[kWarps][32 * VPL];   // scratch of a token's choice
+    __shared__ double s_acc[kWarps][32 * VPL];   // sums of s / sum s, each lane its own
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int N = p.N, k = p.k;
     const int e0 = lane * VPL;
     const bool nodes = p.n_groups > 1;
+    const bool near_matters = nodes || p.bias != nullptr;
     const int per = nodes ? N / p.n_groups : N;
+    const int nl = p.node_lanes;
 
     bool bad = false;
-    float b[VPL];
-    double acc[VPL];
+    float b[VPL], bmax = 0.0f;
+    float part[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         b[i] = (p.bias && e0 + i < N) ? p.bias[e0 + i] : 0.0f;
@@ -121,109 +348,111 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteParams p)
             bad = true;
             b[i] = -INFINITY;
         }
-        acc[i] = 0.0;
+        if (!isinf(b[i]))
+            bmax = fmaxf(bmax, fabsf(b[i]));
+        s_acc[warp][e0 + i] = 0.0;
+        part[i] = 0.0f;
     }
+    // Scores are at most 1 and their 32-bit values within 2^-21 of them (an
+    // exponential and a quotient, each off by a few half steps; a softmax's sum
+    // of up to 256 positive terms); adding the bias is off by 2^-24 of 1 + |b|.
+    // Values more than twice that apart, rounded up, are ordered right.
+    const float margin = 0x1p-19f * (1.0f + warp_max(bmax));
     const int64_t esz = BF16 ? 2 : 4;
     const int64_t nwarps = static_cast<int64_t>(gridDim.x) * kWarps;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < p.T; t += nwarps) {
+    int held = 0;
+    int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    float nxt[VPL];
+    if (t < p.T)
+        load_logits<VPL, BF16>(static_cast<const uint8_t *>(p.logits) + t * p.ld * esz, e0, N,
+                               p.vec, nxt);
+    for (; t < p.T; t += nwarps) {
         const void *row = static_cast<const uint8_t *>(p.logits) + t * p.ld * esz;
         float l[VPL];
         float mx = -INFINITY;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            l[i] = e0 + i < N ? clean_logit(load_logit<BF16>(row, e0 + i), bad) : -INFINITY;
+            l[i] = clean_logit(nxt[i], bad);
             mx = fmaxf(mx, l[i]);
         }
+        if (t + nwarps < p.T)
+            load_logits<VPL, BF16>(static_cast<const uint8_t *>(p.logits) + (t + nwarps) * p.ld * esz,
+                                   e0, N, p.vec, nxt);
         mx = warp_max(mx);
-        double s[VPL], z = 0.0;
+        float s[VPL], z = 0.0f;
+        const bool tiny = !p.softmax && mx < kTinyScore;
+        // s, or up to a factor: e^{l - max} for a softmax and below kTinyScore
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            const double li = l[i];
-            if (l[i] == -INFINITY)
-                s[i] = 0.0;
+            if (p.softmax || tiny)
+                s[i] = l[i] == -INFINITY ? 0.0f : expf(l[i] - mx);
             else
-                s[i] = p.softmax ? exp(li - static_cast<double>(mx)) : 1.0 / (1.0 + exp(-li));
+                s[i] = __fdividef(1.0f, 1.0f + expf(-l[i]));
             z += s[i];
         }
         z = warp_sum(z);
-        double q[VPL];           // s up to a factor that cancels in s / sum s
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            q[i] = s[i];
-        if (!p.softmax && mx < kTinyScore && mx != -INFINITY) {
-            z = 0.0;
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                q[i] = exp(static_cast<double>(l[i]) - static_cast<double>(mx));
-                z += q[i];
-            }
-            z = warp_sum(z);
-        }
-        const double rz = z > 0.0 ? 1.0 / z : 0.0;
-        uint64_t key[VPL];
+        const float rz = z > 0.0f ? __frcp_rn(z) : 0.0f;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            const double sn = q[i] * rz;
-            acc[i] += sn;
+            const float q = s[i] * rz;
+            part[i] += q;
             if (p.softmax)
-                s[i] = sn;
-            const bool off = l[i] == -INFINITY || b[i] == -INFINITY;
-            const double v = s[i] + static_cast<double>(b[i]);
-            if (nodes)
-                s_val[warp][e0 + i] = off ? -INFINITY : v;
-            key[i] = e0 + i >= N ? 0ull
-                                 : (off ? 1ull : order_key(p.bias ? v : static_cast<double>(l[i])));
+                s[i] = q;
         }
-        if (nodes) {
-            // lane g sums the group_top largest values of node g, largest first
-            __syncwarp();
-            uint64_t gkey = 0;
-            if (lane < p.n_groups) {
-                double sum = 0.0, last = INFINITY;
-                int taken_at_last = 0;      // how many equal to `last` have been taken
-                for (int r = 0; r < p.group_top; ++r) {
-                    double best = -INFINITY;
-                    int equal = 0;
-                    for (int i = 0; i < per; ++i) {
-                        const double v = s_val[warp][lane * per + i];
-                        if (v == last)
-                            ++equal;
-                        else if (v < last && v > best)
-                            best = v;
-                    }
-                    if (r > 0 && equal > taken_at_last) {
-                        best = last;
-                        ++taken_at_last;
-                    } else if (r == 0 && equal > 0) {      // values of +inf
-                        best = last;
-                        taken_at_last = 1;
-                    } else {
-                        last = best;
-                        taken_at_last = 1;
-                    }
-                    if (best == -INFINITY)
-                        break;
-                    sum += best;
-                }
-                gkey = order_key(sum);
-            }
-            uint32_t chosen = 0;
-            for (int r = 0; r < p.topk_groups; ++r) {
-                const uint64_t m = warp_key_max(gkey);
-                const int g = __ffs(__ballot_sync(kAll, gkey == m)) - 1;
-                chosen |= 1u << g;
-                if (lane == g)
-                    gkey = 0;
-            }
+        if (++held == 32) {          // 32-bit sums of 32 tokens, then 64
+            held = 0;
 #pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                if (e0 + i < N && !((chosen >> ((e0 + i) / per)) & 1u))
-                    key[i] = 0;
-            __syncwarp();
+            for (int i = 0; i < VPL; ++i) {
+                s_acc[warp][e0 + i] += part[i];
+                part[i] = 0.0f;
+            }
         }
         int mine = 0;
-        for (int j = 0; j < k; ++j) {
-            uint64_t best = 0;
+        bool exact = near_matters && (tiny || p.group_top > 4);
+        if (!exact) {
+            uint32_t key[VPL];
+            float v[VPL];
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                const bool off = l[i] == -INFINITY || b[i] == -INFINITY;
+                v[i] = off ? -INFINITY : s[i] + b[i];
+                key[i] = e0 + i >= N ? 0u : (off ? 1u : order_key(p.bias ? v[i] : l[i]));
+            }
+            if (nodes) {
+                const float *s_node = nullptr;
+                float *sv = reinterpret_cast<float *>(s_val[warp]);
+                int count = 0;
+                const int g = lane / nl;
+                if (!p.node_direct) {
+#pragma unroll
+                    for (int i = 0; i < VPL; ++i)
+                        sv[e0 + i] = v[i];
+                    __syncwarp();
+                    s_node = sv + (g < p.n_groups ? g * per + lane % nl : 0);
+                    count = g < p.n_groups ? (per - lane % nl + nl - 1) / nl : 0;
+                }
+                const float sum = p.group_top <= 2
+                                      ? node_sum<2, VPL>(v, s_node, count, nl, p.group_top)
+                                      : node_sum<4, VPL>(v, s_node, count, nl, p.group_top);
+                uint32_t gkey = g < p.n_groups && lane % nl == 0 ? order_key(sum) : 0u;
+                uint32_t chosen = 0, m = 0;
+                for (int r = 0; r < p.topk_groups; ++r) {
+                    m = __reduce_max_sync(kAll, gkey);
+                    const int src = __ffs(__ballot_sync(kAll, gkey == m)) - 1;
+                    chosen |= 1u << (src / nl);
+                    if (lane == src)
+                        gkey = 0;
+                }
+                const uint32_t next = __reduce_max_sync(kAll, gkey);
+                exact = !(key_value(m) - key_value(next) > 4.0f * margin);
+#pragma unroll
+                for (int i = 0; i < VPL; ++i)
+                    if (e0 + i < N && !((chosen >> ((e0 + i) / per)) & 1u))
+                        key[i] = 0;
+                __syncwarp();
+            }
+            // the best of each lane; the winner's lane looks again
+            uint32_t best = 0;
             int bi = 0;
 #pragma unroll
             for (int i = 0; i < VPL; ++i)
@@ -231,55 +460,85 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteParams p)
                     best = key[i];
                     bi = i;
                 }
-            const uint64_t m = warp_key_max(best);
-            const int src = __ffs(__ballot_sync(kAll, best == m)) - 1;
-            const int e = __shfl_sync(kAll, e0 + bi, src);
-            if (lane == src) {
+            uint32_t my_key = 0;
+            const int rounds = p.bias && k < N ? k + 1 : k;
+            for (int j = 0; j < rounds; ++j) {
+                const uint32_t m = __reduce_max_sync(kAll, best);
+                const int src = __ffs(__ballot_sync(kAll, best == m)) - 1;
+                const int e = __shfl_sync(kAll, e0 + bi, src);
+                if (lane == j) {
+                    mine = e;
+                    my_key = m;
+                }
+                if (lane == src) {
+                    best = 0;
+                    const int gone = bi;
 #pragma unroll
-                for (int i = 0; i < VPL; ++i)
-                    if (i == bi)
-                        key[i] = 0;
+                    for (int i = 0; i < VPL; ++i) {
+                        if (i == gone)
+                            key[i] = 0;
+                        if (key[i] > best) {
+                            best = key[i];
+                            bi = i;
+                        }
+                    }
+                }
             }
-            if (lane == j)
-                mine = e;
+            if (p.bias && !exact) {
+                // each slot against the next one, the last against the first left out
+                const uint32_t nk = __shfl_down_sync(kAll, my_key, 1);
+                const int ne = __shfl_down_sync(kAll, mine, 1);
+                bool close = false;
+                if (lane < k && nk > 1u && !(key_value(my_key) - key_value(nk) > 2.0f * margin)) {
+                    // equal logits with equal biases are equal in every precision
+                    const bool same =
+                        load_logit<BF16>(row, mine) == load_logit<BF16>(row, ne) &&
+                        (!p.bias || p.bias[mine] == p.bias[ne]);
+                    close = !same || my_key != nk;
+                }
+                exact = __any_sync(kAll, close);
+            }
         }
+        if (exact)
+            mine = choose_exact<VPL, BF16>(p, row, s_val[warp]);
         // weights: lane j has expert e_j; renormalised ones up to a common factor
         bool ignore = false;
-        const float le =
-            lane < k ? clean_logit(load_logit<BF16>(row, mine), ignore) : -INFINITY;
-        const float mc = p.renorm ? warp_max(le) : mx;
-        double w = 0.0;
+        const float le = lane < k ? clean_logit(load_logit<BF16>(row, mine), ignore) : -INFINITY;
+        const float mc = p.renorm ? slot_max(le) : mx;
+        float w = 0.0f;
         if (le != -INFINITY) {
             if (p.softmax)
-                w = exp(static_cast<double>(le) - static_cast<double>(mc)) * (p.renorm ? 1.0 : rz);
+                w = expf(le - mc) * (p.renorm ? 1.0f : rz);
             else if (p.renorm && mc < kTinyScore)
-                w = exp(static_cast<double>(le) - static_cast<double>(mc));
+                w = expf(le - mc);
             else
-                w = 1.0 / (1.0 + exp(-static_cast<double>(le)));
+                w = 1.0f / (1.0f + expf(-le));
         }
         if (p.renorm) {
-            const double d = warp_sum(w);
-            w = d > 0.0 ? w / d : 0.0;
+            const float d = slot_sum(w);
+            w = d > 0.0f ? w / d : 0.0f;
         }
         if (lane < k) {
             p.topk_idx[t * k + lane] = mine;
-            p.topk_w[t * k + lane] = static_cast<float>(w * static_cast<double>(p.scale));
+            p.topk_w[t * k + lane] = w * p.scale;
         }
     }
     if (bad)
         set_status(p.status, DEV_NAN_LOGIT);
-    if (p.p_part) {
+    if (p.p_part || p.p_mean) {
         // the block's sums, warp by warp in order
-        __syncthreads();
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
-            s_val[warp][e0 + i] = acc[i];
+            s_acc[warp][e0 + i] += part[i];
         __syncthreads();
         for (int e = threadIdx.x; e < N; e += kThreads) {
             double sum = 0.0;
             for (int w = 0; w < kWarps; ++w)
-                sum += s_val[w][e];
-            p.p_part[static_cast<int64_t>(blockIdx.x) * N + e] = sum;
+                sum += s_acc[w][e];
+            if (p.p_mean)
+                p.p_mean[e] = static_cast<float>(sum / static_cast<double>(p.T));
+            else
+                p.p_part[static_cast<int64_t>(blockIdx.x) * N + e] = sum;
         }
     }
 }
@@ -292,6 +551,7 @@ struct RouteGradParams {
     void *dlogits;
     int64_t T, ld;
     int32_t N, k, softmax, renorm;
+    int32_t vec;             // both matrices' rows start on a lane's vector boundary
     float scale;
     uint32_t *status;
 };
@@ -305,16 +565,55 @@ __device__ __forceinline__ void store_logit(void *row, int e, float v)
         static_cast<float *>(row)[e] = v;
 }
 
+template <int VPL, bool BF16>
+__device__ __forceinline__ void store_logits(void *row, int e0, int N, bool vec,
+                                             const float (&d)[VPL])
+{
+    constexpr int bytes = VPL * (BF16 ? 2 : 4);
+    uint8_t *at = static_cast<uint8_t *>(row) + static_cast<int64_t>(e0) * (BF16 ? 2 : 4);
+    if (VPL >= 4 && vec && e0 + VPL <= N) {
+        uint32_t w[bytes >= 8 ? bytes / 4 : 2];
+#pragma unroll
+        for (int i = 0; i < bytes / 4; ++i)
+            w[i] = BF16 ? pack_bf16x2(d[(2 * i) % VPL], d[(2 * i + 1) % VPL]) : __float_as_uint(d[i % VPL]);
+        if (bytes >= 16) {
+#pragma unroll
+            for (int i = 0; i < bytes / 16; ++i)
+                reinterpret_cast<uint4 *>(at)[i] =
+                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        } else {
+            *reinterpret_cast<uint2 *>(at) = make_uint2(w[0], w[1]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (e0 + i < N)
+                store_logit<BF16>(row, e0 + i, d[i]);
+    }
+}
+
+// s and 1 - s of the logistic function, both without cancellation.
+__device__ __forceinline__ void logistic(float l, float &s, float &om)
+{
+    const float t = expf(-fabsf(l));
+    const float r = __fdividef(1.0f, 1.0f + t);
+    const float tr = t * r;
+    s = l > 0.0f ? r : tr;
+    om = l > 0.0f ? tr : r;
+}
+
 // With c = dp_mean / T, q = s / sum s, g = scale * dtopk_w, and over the
 // chosen slots r = s / sum s (renormalised):
 //   sigmoid: dl_e = (1 - s_e) * (q_e (c_e - sum c q) + [e chosen] u_e),
 //            u = r (g - sum g r) renormalised, else s g
 //   softmax: dl_e = p_e (c_e - sum c p) + [e chosen] u_e (- p_e sum g p),
 //            u = r (g - sum g r) renormalised, else p g (and the last term)
-// The sigmoid's ratios are formed from e^{l - m} / (1 + e^l) with m the
-// smaller of 0 and the largest logit, so they neither under- nor overflow.
+// Ratios of scores below kTinyScore are formed from e^{l - max}, so they do
+// not underflow.  One warp per token: the logits are read once and the
+// gradient is written once (2 T N values, the bound by bytes), the k chosen
+// experts' gradients a second time by the lanes that hold the slots.
 template <int VPL, bool BF16>
-__global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteGradParams p)
+__global__ void __launch_bounds__(kThreads) route_grad_kernel(const __grid_constant__ RouteGradParams p)
 {
     grid_dep_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -328,103 +627,110 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteGradParams p)
     const int64_t esz = BF16 ? 2 : 4;
     const int64_t nwarps = static_cast<int64_t>(gridDim.x) * kWarps;
     bool bad = false, nan = false;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < p.T; t += nwarps) {
+    int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    float nxt[VPL];
+    int nme = -1;
+    float ng = 0.0f;
+    auto fetch = [&](int64_t at) {
+        load_logits<VPL, BF16>(static_cast<const uint8_t *>(p.logits) + at * p.ld * esz, e0, N,
+                               p.vec, nxt);
+        if (lane < k && p.dtopk_w) {
+            nme = p.topk_idx[at * k + lane];
+            ng = p.dtopk_w[at * k + lane];
+        }
+    };
+    if (t < p.T)
+        fetch(t);
+    for (; t < p.T; t += nwarps) {
         const void *row = static_cast<const uint8_t *>(p.logits) + t * p.ld * esz;
         void *out = static_cast<uint8_t *>(p.dlogits) + t * p.ld * esz;
         // chosen slots, one per lane
         int me = -1;
-        float lc = -INFINITY, g = 0.0f;
+        float lc = -INFINITY, cm = 0.0f;
+        const float g = p.scale * ng;
         if (lane < k && p.dtopk_w) {
-            me = p.topk_idx[t * k + lane];
-            if (me < 0 || me >= N) {
+            if (nme < 0 || nme >= N) {
                 bad = true;
-                me = -1;
             } else {
+                me = nme;
                 lc = clean_logit(load_logit<BF16>(row, me), nan);
-                g = p.scale * p.dtopk_w[t * k + lane];
+                if (p.dp_mean)
+                    cm = p.dp_mean[me] * inv_t;
             }
         }
         float l[VPL], mx = -INFINITY;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            l[i] = e0 + i < N ? clean_logit(load_logit<BF16>(row, e0 + i), nan) : -INFINITY;
+            l[i] = clean_logit(nxt[i], nan);
             mx = fmaxf(mx, l[i]);
         }
-        mx = warp_max(mx);
-        const float m = p.softmax ? mx : fminf(mx, 0.0f);
-        // s up to the factor that cancels in q
-        float s[VPL], z = 0.0f, cz = 0.0f;
+        if (t + nwarps < p.T)
+            fetch(t + nwarps);
+        // the shift of the exponentials: none for the logistic function unless it is tiny
+        const bool tiny = !p.softmax && warp_max(mx) < kTinyScore;
+        mx = (p.softmax || tiny) ? warp_max(mx) : 0.0f;
+        float s[VPL], om[VPL], z = 0.0f, cz = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            if (l[i] == -INFINITY)
-                s[i] = 0.0f;
-            else if (p.softmax)
-                s[i] = expf(l[i] - m);
+            om[i] = 1.0f;
+            if (p.softmax || tiny)
+                s[i] = l[i] == -INFINITY ? 0.0f : expf(l[i] - mx);
             else
-                s[i] = l[i] > 0.0f ? 1.0f / (1.0f + expf(-l[i]))
-                                   : expf(l[i] - m) / (1.0f + expf(l[i]));
+                logistic(l[i], s[i], om[i]);
             z += s[i];
             cz = fmaf(c[i], s[i], cz);
         }
         z = warp_sum(z);
-        cz = warp_sum(cz);
-        const float rz = z > 0.0f ? 1.0f / z : 0.0f;
+        if (p.dp_mean)
+            cz = warp_sum(cz);
+        const float rz = z > 0.0f ? __frcp_rn(z) : 0.0f;
         const float cq = cz * rz;
-        // chosen: u, and for plain softmax sum g p
-        const float mc = warp_max(lc);
-        float sc = 0.0f, om = 0.0f;     // score (up to a factor when renormalised), 1 - s
+        // chosen: score (up to a factor when renormalised), 1 - s, share of the row's sum
+        float sc = 0.0f, oc = 1.0f, share = 0.0f;
+        const float mc = p.renorm ? slot_max(lc) : mx;
         if (lc != -INFINITY) {
-            const float shift = p.renorm ? (p.softmax ? mc : fminf(mc, 0.0f)) : (p.softmax ? mx : 0.0f);
-            if (p.softmax) {
-                sc = expf(lc - shift) * (p.renorm ? 1.0f : rz);
+            if (p.softmax || (p.renorm && mc < kTinyScore))
+                sc = expf(lc - mc) * (p.renorm ? 1.0f : rz);
+            else
+                logistic(lc, sc, oc);
+            if (p.softmax || tiny) {
+                share = expf(lc - mx) * rz;
             } else {
-                sc = lc > 0.0f ? 1.0f / (1.0f + expf(-lc)) : expf(lc - shift) / (1.0f + expf(lc));
-                om = 1.0f / (1.0f + expf(lc));
+                float so;
+                logistic(lc, so, oc);
+                share = so * rz;
             }
         }
         float u, gp = 0.0f;
         if (p.renorm) {
-            const float d = warp_sum(sc);
-            const float r = d > 0.0f ? sc / d : 0.0f;
-            u = r * (g - warp_sum(r * g));
+            const float d = slot_sum(sc);
+            const float r = d > 0.0f ? __fdividef(sc, d) : 0.0f;
+            u = r * (g - slot_sum(r * g));
         } else {
             u = sc * g;
             if (p.softmax)
-                gp = warp_sum(u);
+                gp = __shfl_sync(kAll, slot_sum(u), 0);
         }
-        if (!p.softmax)
-            u *= om;
-        // base gradient of every expert
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            if (e0 + i >= N)
-                continue;
-            float d = s[i] * rz * (c[i] - cq - gp);
-            if (!p.softmax && l[i] != -INFINITY)
-                d *= 1.0f / (1.0f + expf(l[i]));
-            store_logit<BF16>(out, e0 + i, l[i] == -INFINITY ? 0.0f : d);
-        }
-        // the chosen experts again, with their slots' share
+        // the same expert in several slots adds up
         float us = 0.0f;
-        for (int j = 0; j < k; ++j) {
-            const int ej = __shfl_sync(kAll, me, j);
-            const float uj = __shfl_sync(kAll, u, j);
-            if (ej == me)
-                us += uj;
+        if (p.dtopk_w) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int ej = __shfl_sync(kAll, me, j);
+                const float uj = __shfl_sync(kAll, u, j);
+                us += ej == me ? uj : 0.0f;
+            }
         }
+        // every expert without its slots' share, then the chosen ones with it
+        const float sub = cq + gp;
+        float d[VPL];
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            d[i] = s[i] * rz * (c[i] - sub) * om[i];
+        store_logits<VPL, BF16>(out, e0, N, p.vec, d);
         __syncwarp();
-        if (me >= 0) {
-            float sb = 0.0f;
-            if (lc != -INFINITY)
-                sb = p.softmax ? expf(lc - m)
-                               : (lc > 0.0f ? 1.0f / (1.0f + expf(-lc)) : expf(lc - m) / (1.0f + expf(lc)));
-            const float cm = p.dp_mean ? p.dp_mean[me] * inv_t : 0.0f;
-            float d = sb * rz * (cm - cq - gp);
-            if (!p.softmax)
-                d *= om;
-            store_logit<BF16>(out, me, lc == -INFINITY ? 0.0f : d + us);
-        }
-        __syncwarp();
+        if (me >= 0)
+            store_logit<BF16>(out, me, lc == -INFINITY ? 0.0f : oc * (share * (cm - sub) + us));
     }
     if (bad)
         set_status(p.status, DEV_BAD_EXPERT);
@@ -444,18 +750,25 @@ int route_grid(int64_t T)
     return static_cast<int>(g < cap ? g : cap);
 }
 
+// Whether every row of [T, ld] logits starts on a boundary of 16 bytes.
+bool rows_on_16(const void *base, int64_t ld, int dtype)
+{
+    const int64_t es = dtype == MOE_BF16 ? 2 : 4;
+    return reinterpret_cast<uintptr_t>(base) % 16 == 0 && (ld * es) % 16 == 0;
+}
+
+int lane_values(int N) { return N <= 32 ? 1 : (N <= 64 ? 2 : (N <= 128 ? 4 : 8)); }
+
 // Calls f with the kernel variant's values per lane as a constant.
 template <typename F>
 void with_vpl(int N, F f)
 {
-    if (N <= 32)
-        f(std::integral_constant<int, 1>());
-    else if (N <= 64)
-        f(std::integral_constant<int, 2>());
-    else if (N <= 128)
-        f(std::integral_constant<int, 4>());
-    else
-        f(std::integral_constant<int, 8>());
+    switch (lane_values(N)) {
+    case 1: f(std::integral_constant<int, 1>()); break;
+    case 2: f(std::integral_constant<int, 2>()); break;
+    case 4: f(std::integral_constant<int, 4>()); break;
+    default: f(std::integral_constant<int, 8>()); break;
+    }
 }
 
 }  // namespace
@@ -477,9 +790,29 @@ cudaError_t launch_route(const RouteLaunch &L, cudaStream_t stream)
     p.scale = L.scale;
     p.topk_idx = L.topk_idx;
     p.topk_w = L.topk_w;
-    p.p_part = L.p_mean ? L.p_part : nullptr;
     p.status = L.status;
+    p.vec = rows_on_16(L.logits, L.ld, L.dtype);
+    p.node_lanes = 1;
+    p.node_direct = 0;
+    if (L.n_groups > 1) {
+        // a node's values lie on whole lanes, a power of two of them, or are
+        // gathered onto 32 / n_groups lanes
+        const int v = lane_values(L.N), per = L.N / L.n_groups;
+        const int lanes = per / v;
+        if (per % v == 0 && (lanes & (lanes - 1)) == 0) {
+            p.node_lanes = lanes;
+            p.node_direct = 1;
+        } else {
+            int lg = 32;
+            while (lg * L.n_groups > 32)
+                lg >>= 1;
+            p.node_lanes = lg;
+        }
+    }
     const int grid = route_grid(L.T);
+    // one block writes its sums as the result
+    p.p_mean = grid == 1 ? L.p_mean : nullptr;
+    p.p_part = L.p_mean && grid > 1 ? L.p_part : nullptr;
     with_vpl(L.N, [&](auto v) {
         constexpr int VPL = decltype(v)::value;
         if (L.dtype == MOE_BF16)
@@ -489,7 +822,7 @@ cudaError_t launch_route(const RouteLaunch &L, cudaStream_t stream)
     });
     count_launches(1);
     const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || !L.p_mean)
+    if (e != cudaSuccess || !p.p_part)
         return e;
     return launch_p_finalize(L.p_part, grid, L.N, L.T, L.p_mean, stream);
 }
@@ -510,6 +843,7 @@ cudaError_t launch_route_grad(const RouteGradLaunch &L, cudaStream_t stream)
     p.renorm = L.renormalize;
     p.scale = L.scale;
     p.status = L.status;
+    p.vec = rows_on_16(L.logits, L.ld, L.dtype) && rows_on_16(L.dlogits, L.ld, L.dtype);
     const int grid = route_grid(L.T);
     with_vpl(L.N, [&](auto v) {
         constexpr int VPL = decltype(v)::value;
