@@ -37,6 +37,8 @@ struct RouteParams {
     int32_t vec;             // rows start on a lane's vector boundary
     int32_t node_lanes;      // lanes that hold a node's values
     int32_t node_direct;     // 1: in the order they are loaded in (else regathered)
+    int32_t per_node;
+    int32_t want_p;
     float scale;
     int32_t *topk_idx;
     float *topk_w;
@@ -106,11 +108,8 @@ __device__ __forceinline__ float warp_max(float v)
 // The logit as it counts: NaN as -inf (reported), +inf as the largest finite.
 __device__ __forceinline__ float clean_logit(float l, bool &nan)
 {
-    if (isnan(l)) {
-        nan = true;
-        return -INFINITY;
-    }
-    return fminf(l, FLT_MAX);
+    nan |= l != l;
+    return fminf(fmaxf(l, -INFINITY), FLT_MAX);      // the maximum with a NaN is the other operand
 }
 
 template <bool BF16>
@@ -156,20 +155,234 @@ __device__ __forceinline__ void load_logits(const void *row, int e0, int N, bool
     }
 }
 
+// e^x in 64 bits within 2 ulp, for x <= 0: x = n ln 2 + r with |r| <= ln 2 / 2,
+// the Taylor series of e^r to r^13 / 13! (the next term is below 2^-57), scaled
+// by 2^n.  Inlined, so a lane's series run side by side; below -708: 0.
+__device__ __forceinline__ double exp_64(double x)
+{
+    const double n = rint(x * 1.4426950408889634);
+    double r = fma(n, -0.69314718055994529, x);
+    r = fma(n, -2.3190468138462996e-17, r);
+    double e = 1.0 / 6227020800.0;
+    constexpr double f[13] = {1.0 / 479001600.0, 1.0 / 39916800.0, 1.0 / 3628800.0, 1.0 / 362880.0,
+                              1.0 / 40320.0, 1.0 / 5040.0, 1.0 / 720.0, 1.0 / 120.0, 1.0 / 24.0,
+                              1.0 / 6.0, 0.5, 1.0, 1.0};
+#pragma unroll
+    for (int i = 0; i < 13; ++i)
+        e = fma(e, r, f[i]);
+    const double p = __hiloint2double((static_cast<int>(fmax(n, -1022.0)) + 1023) << 20, 0);
+    return x < -708.0 ? 0.0 : e * p;
+}
+
+// 1 / x in 64 bits within 2 ulp, for 1 <= x <= 2: Newton's iteration from the
+// 32-bit reciprocal (each doubles the right bits).
+__device__ __forceinline__ double recip_64(double x)
+{
+    double y = static_cast<double>(__frcp_rn(static_cast<float>(x)));
+    y = fma(y, fma(-x, y, 1.0), y);
+    return fma(y, fma(-x, y, 1.0), y);
+}
+
+__device__ __forceinline__ uint32_t key_max(uint32_t v) { return __reduce_max_sync(kAll, v); }
+__device__ __forceinline__ uint64_t key_max(uint64_t v) { return warp_key_max(v); }
+
+// Inserts v into a list of the M largest values, largest first.
+template <int M, typename F>
+__device__ __forceinline__ void list_insert(F (&a)[M], F v)
+{
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+        const F hi = v > a[i] ? v : a[i];
+        v = v > a[i] ? a[i] : v;
+        a[i] = hi;
+    }
+}
+
+// Sum of the `m` (at most M) largest of the values of this lane's node, on
+// every lane of the node, largest first; -inf counts as nothing.  The lists of
+// two halves of a node merge entry by entry.
+template <int M, int VPL, typename F>
+__device__ __forceinline__ F node_sum(const F (&v)[VPL], const F *s_node, int count, int lanes,
+                                      int m)
+{
+    F a[M];
+#pragma unroll
+    for (int i = 0; i < M; ++i)
+        a[i] = -INFINITY;
+    if (s_node) {
+        for (int i = 0; i < count; ++i)
+            list_insert<M, F>(a, s_node[i * lanes]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            list_insert<M, F>(a, v[i]);
+    }
+    for (int o = 1; o < lanes; o <<= 1) {
+        F b[M];
+#pragma unroll
+        for (int i = 0; i < M; ++i)
+            b[i] = __shfl_xor_sync(kAll, a[i], o);
+#pragma unroll
+        for (int i = 0; i < M; ++i)
+            list_insert<M, F>(a, b[i]);
+    }
+    F sum = 0;
+#pragma unroll
+    for (int i = 0; i < M; ++i)
+        if (i < m && a[i] != -INFINITY)
+            sum += a[i];
+    return sum;
+}
+
+// Sum of the `m` largest of `per` values in shared memory, for any m: each
+// pass finds the largest one below the last taken (or one more equal to it).
+template <typename F>
+__device__ __forceinline__ F node_sum_any(const F *v, int per, int m)
+{
+    F sum = 0, last = INFINITY;
+    int taken = 0;              // of the values equal to `last`
+    for (int r = 0; r < m; ++r) {
+        F best = -INFINITY;
+        int equal = 0;
+        for (int i = 0; i < per; ++i) {
+            if (v[i] == last)
+                ++equal;
+            else if (v[i] < last && v[i] > best)
+                best = v[i];
+        }
+        if (equal > taken) {
+            best = last;
+            ++taken;
+        } else {
+            last = best;
+            taken = 1;
+        }
+        if (best == -INFINITY)
+            break;
+        sum += best;
+    }
+    return sum;
+}
+
+__device__ __forceinline__ float key_value_of(uint32_t k) { return key_value(k); }
+__device__ __forceinline__ double key_value_of(uint64_t k)
+{
+    return __longlong_as_double(static_cast<long long>((k >> 63) ? (k & 0x7FFFFFFFFFFFFFFFull) : ~k));
+}
+
+// The choice: v = s + b of this lane's experts (-inf: switched off), K the key
+// type of F.  Lane j < k gets its slot's expert in `mine`, lane j <= rounds - 1
+// the key it won with in `my_key`.  Returns whether a chosen node's score is
+// within node_margin of the first one left out.
+template <typename F, typename K, int VPL>
+__device__ __forceinline__ bool choose(const RouteParams &p, const F (&v)[VPL],
+                                       const float (&l)[VPL], F *scratch, F node_margin,
+                                       int rounds, int &mine, K &my_key)
+{
+    const int lane = threadIdx.x & 31;
+    const int e0 = lane * VPL;
+    const int N = p.N;
+    bool near = false;
+    K key[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+        key[i] = e0 + i >= N ? K(0)
+                             : (v[i] == -INFINITY ? K(1)
+                                                  : order_key(p.bias ? v[i] : static_cast<F>(l[i])));
+    if (p.n_groups > 1) {
+        const int nl = p.node_lanes, per = p.per_node;
+        const int g = lane / nl;
+        const F *s_node = nullptr;
+        int count = 0;
+        if (!p.node_direct) {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                scratch[e0 + i] = v[i];
+            __syncwarp();
+            const int at = lane - g * nl;
+            s_node = scratch + (g < p.n_groups ? g * per + at : 0);
+            count = g < p.n_groups ? (per - at + nl - 1) / nl : 0;
+        }
+        F sum;
+        if (p.group_top <= 2)
+            sum = node_sum<2, VPL, F>(v, s_node, count, nl, p.group_top);
+        else if (p.group_top <= 4)
+            sum = node_sum<4, VPL, F>(v, s_node, count, nl, p.group_top);
+        else
+            sum = node_sum_any<F>(scratch + (g < p.n_groups ? g * per : 0),
+                                  g < p.n_groups ? per : 0, p.group_top);
+        K gkey = g < p.n_groups && lane == g * nl ? order_key(sum) : K(0);
+        uint32_t chosen = 0;
+        K m = 0;
+        for (int r = 0; r < p.topk_groups; ++r) {
+            m = key_max(gkey);
+            const int src = __ffs(__ballot_sync(kAll, gkey == m)) - 1;
+            chosen |= 1u << (src / nl);
+            if (lane == src)
+                gkey = 0;
+        }
+        near = !(key_value_of(m) - key_value_of(key_max(gkey)) > node_margin);
+        if (p.node_direct) {
+            if (!((chosen >> g) & 1u)) {
+#pragma unroll
+                for (int i = 0; i < VPL; ++i)
+                    key[i] = 0;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if (e0 + i < N && !((chosen >> ((e0 + i) / per)) & 1u))
+                    key[i] = 0;
+            __syncwarp();
+        }
+    }
+    // the best of each lane; the winner's lane looks again
+    K best = 0;
+    int bi = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+        if (key[i] > best) {
+            best = key[i];
+            bi = i;
+        }
+    my_key = 0;
+    mine = 0;
+    for (int j = 0; j < rounds; ++j) {
+        const K m = key_max(best);
+        const int src = __ffs(__ballot_sync(kAll, best == m)) - 1;
+        const int e = __shfl_sync(kAll, e0 + bi, src);
+        if (lane == j) {
+            mine = e;
+            my_key = m;
+        }
+        if (lane == src && j + 1 < rounds) {
+            best = 0;
+            const int gone = bi;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                if (i == gone)
+                    key[i] = 0;
+                if (key[i] > best) {
+                    best = key[i];
+                    bi = i;
+                }
+            }
+        }
+    }
+    return near;
+}
+
 // The choice in 64 bits, from the logits: the index of lane j's slot (lanes
-// below k).  Taken for tokens whose 32-bit values are too near one another
-// (route_kernel), and for nodes of more than 4 summed values.  s_val: 256
-// doubles of this warp.
-template <int VPL, bool BF16>
+// below k).  Taken for tokens whose 32-bit values are too near one another.
+// s_val: doubles of this warp.
+template <int VPL, bool BF16, bool SOFTMAX>
 __device__ __noinline__ int choose_exact(const RouteParams &p, const void *row, double *s_val)
 {
     const int lane = threadIdx.x & 31;
-    const int N = p.N;
     const int e0 = lane * VPL;
-    const bool nodes = p.n_groups > 1;
     bool ignore = false;
     float l[VPL], mx = -INFINITY;
-    load_logits<VPL, BF16>(row, e0, N, p.vec, l);
+    load_logits<VPL, BF16>(row, e0, p.N, p.vec, l);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         l[i] = clean_logit(l[i], ignore);
@@ -180,142 +393,31 @@ __device__ __noinline__ int choose_exact(const RouteParams &p, const void *row, 
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         const double li = l[i];
-        if (l[i] == -INFINITY)
-            s[i] = 0.0;
-        else
-            s[i] = p.softmax ? exp(li - static_cast<double>(mx)) : 1.0 / (1.0 + exp(-li));
-        z += s[i];
+        if (SOFTMAX) {
+            s[i] = l[i] == -INFINITY ? 0.0 : exp_64(li - static_cast<double>(mx));
+            z += s[i];
+        } else {
+            const double t = exp_64(-fabs(li));
+            const double r = recip_64(1.0 + t);
+            s[i] = l[i] > 0.0f ? r : t * r;
+        }
     }
-    z = warp_sum(z);
-    const double rz = p.softmax && z > 0.0 ? 1.0 / z : 1.0;
-    uint64_t key[VPL];
+    if (SOFTMAX) {
+        z = warp_sum(z);
+        z = z > 0.0 ? 1.0 / z : 0.0;
+    }
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-        float b = (p.bias && e0 + i < N) ? p.bias[e0 + i] : 0.0f;
-        b = isnan(b) ? -INFINITY : b;
-        const bool off = l[i] == -INFINITY || b == -INFINITY;
-        const double v = s[i] * rz + static_cast<double>(b);
-        if (nodes)
-            s_val[e0 + i] = off ? -INFINITY : v;
-        key[i] = e0 + i >= N ? 0ull
-                             : (off ? 1ull : order_key(p.bias ? v : static_cast<double>(l[i])));
+        float b = (p.bias && e0 + i < p.N) ? p.bias[e0 + i] : 0.0f;
+        b = fmaxf(b, -INFINITY);
+        if (SOFTMAX)
+            s[i] *= z;
+        s[i] = l[i] == -INFINITY || b == -INFINITY ? -INFINITY : s[i] + static_cast<double>(b);
     }
-    if (nodes) {
-        // lane g sums the group_top largest values of node g, largest first
-        __syncwarp();
-        const int per = N / p.n_groups;
-        uint64_t gkey = 0;
-        if (lane < p.n_groups) {
-            double sum = 0.0, last = INFINITY;
-            int taken = 0;              // of the values equal to `last`
-            for (int r = 0; r < p.group_top; ++r) {
-                double best = -INFINITY;
-                int equal = 0;
-                for (int i = 0; i < per; ++i) {
-                    const double v = s_val[lane * per + i];
-                    if (v == last)
-                        ++equal;
-                    else if (v < last && v > best)
-                        best = v;
-                }
-                if (equal > taken) {
-                    best = last;
-                    ++taken;
-                } else {
-                    last = best;
-                    taken = 1;
-                }
-                if (best == -INFINITY)
-                    break;
-                sum += best;
-            }
-            gkey = order_key(sum);
-        }
-        uint32_t chosen = 0;
-        for (int r = 0; r < p.topk_groups; ++r) {
-            const uint64_t m = warp_key_max(gkey);
-            const int g = __ffs(__ballot_sync(kAll, gkey == m)) - 1;
-            chosen |= 1u << g;
-            if (lane == g)
-                gkey = 0;
-        }
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (e0 + i < N && !((chosen >> ((e0 + i) / per)) & 1u))
-                key[i] = 0;
-        __syncwarp();
-    }
-    int mine = 0;
-    for (int j = 0; j < p.k; ++j) {
-        uint64_t best = 0;
-        int bi = 0;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                bi = i;
-            }
-        const uint64_t m = warp_key_max(best);
-        const int src = __ffs(__ballot_sync(kAll, best == m)) - 1;
-        const int e = __shfl_sync(kAll, e0 + bi, src);
-        if (lane == src) {
-#pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                if (i == bi)
-                    key[i] = 0;
-        }
-        if (lane == j)
-            mine = e;
-    }
+    int mine;
+    uint64_t won;
+    choose<double, uint64_t, VPL>(p, s, l, s_val, 0.0, p.k, mine, won);
     return mine;
-}
-
-// Inserts v into a list of the M largest values, largest first.
-template <int M>
-__device__ __forceinline__ void list_insert(float (&a)[M], float v)
-{
-#pragma unroll
-    for (int i = 0; i < M; ++i) {
-        const float hi = fmaxf(a[i], v);
-        v = fminf(a[i], v);
-        a[i] = hi;
-    }
-}
-
-// Sum of the `m` (at most M) largest of the values of this lane's node, on
-// every lane of the node; -inf counts as nothing.  The lists of two halves of
-// a node merge entry by entry.
-template <int M, int VPL>
-__device__ __forceinline__ float node_sum(const float (&v)[VPL], const float *s_node, int count,
-                                          int lanes, int m)
-{
-    float a[M];
-#pragma unroll
-    for (int i = 0; i < M; ++i)
-        a[i] = -INFINITY;
-    if (s_node) {
-        for (int i = 0; i < count; ++i)
-            list_insert<M>(a, s_node[i * lanes]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            list_insert<M>(a, v[i]);
-    }
-    for (int o = 1; o < lanes; o <<= 1) {
-        float b[M];
-#pragma unroll
-        for (int i = 0; i < M; ++i)
-            b[i] = __shfl_xor_sync(kAll, a[i], o);
-#pragma unroll
-        for (int i = 0; i < M; ++i)
-            list_insert<M>(a, b[i]);
-    }
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < M; ++i)
-        if (i < m && a[i] != -INFINITY)
-            sum += a[i];
-    return sum;
 }
 
 // One warp per token, VPL consecutive experts per lane.  What bounds it is the
@@ -324,8 +426,9 @@ __device__ __forceinline__ float node_sum(const float (&v)[VPL], const float *s_
 // decisions hang on differences near the 32-bit error is decided again in
 // 64 (choose_exact).  Without a bias and nodes the 32-bit keys are the logits
 // themselves and decide exactly.
-template <int VPL, bool BF16>
-__global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__ RouteParams p)
+template <int VPL, bool BF16, bool SOFTMAX>
+__global__ void __launch_bounds__(kThreads, VPL == 8 ? 3 : 4)
+    route_kernel(const __grid_constant__ RouteParams p)
 {
     grid_dep_wait();
     __shared__ double s_val[kWarps][32 * VPL];   // scratch of a token's choice
@@ -333,10 +436,7 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int N = p.N, k = p.k;
     const int e0 = lane * VPL;
-    const bool nodes = p.n_groups > 1;
-    const bool near_matters = nodes || p.bias != nullptr;
-    const int per = nodes ? N / p.n_groups : N;
-    const int nl = p.node_lanes;
+    const bool values = p.bias != nullptr || p.n_groups > 1;   // the choice needs s + b
 
     bool bad = false;
     float b[VPL], bmax = 0.0f;
@@ -344,10 +444,8 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         b[i] = (p.bias && e0 + i < N) ? p.bias[e0 + i] : 0.0f;
-        if (isnan(b[i])) {
-            bad = true;
-            b[i] = -INFINITY;
-        }
+        bad |= b[i] != b[i];
+        b[i] = fmaxf(b[i], -INFINITY);
         if (!isinf(b[i]))
             bmax = fmaxf(bmax, fabsf(b[i]));
         s_acc[warp][e0 + i] = 0.0;
@@ -358,16 +456,17 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
     // of up to 256 positive terms); adding the bias is off by 2^-24 of 1 + |b|.
     // Values more than twice that apart, rounded up, are ordered right.
     const float margin = 0x1p-19f * (1.0f + warp_max(bmax));
-    const int64_t esz = BF16 ? 2 : 4;
-    const int64_t nwarps = static_cast<int64_t>(gridDim.x) * kWarps;
-    int held = 0;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
+    const int64_t row_bytes = p.ld * (BF16 ? 2 : 4);
+    const int64_t row_step = step * row_bytes;
     int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    const uint8_t *row = static_cast<const uint8_t *>(p.logits) + t * row_bytes;
+    int64_t slot = t * k + lane;
+    int held = 0;
     float nxt[VPL];
     if (t < p.T)
-        load_logits<VPL, BF16>(static_cast<const uint8_t *>(p.logits) + t * p.ld * esz, e0, N,
-                               p.vec, nxt);
-    for (; t < p.T; t += nwarps) {
-        const void *row = static_cast<const uint8_t *>(p.logits) + t * p.ld * esz;
+        load_logits<VPL, BF16>(row, e0, N, p.vec, nxt);
+    for (; t < p.T; t += step, row += row_step, slot += step * k) {
         float l[VPL];
         float mx = -INFINITY;
 #pragma unroll
@@ -375,29 +474,37 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
             l[i] = clean_logit(nxt[i], bad);
             mx = fmaxf(mx, l[i]);
         }
-        if (t + nwarps < p.T)
-            load_logits<VPL, BF16>(static_cast<const uint8_t *>(p.logits) + (t + nwarps) * p.ld * esz,
-                                   e0, N, p.vec, nxt);
+        if (t + step < p.T)
+            load_logits<VPL, BF16>(row + row_step, e0, N, p.vec, nxt);
         mx = warp_max(mx);
-        float s[VPL], z = 0.0f;
-        const bool tiny = !p.softmax && mx < kTinyScore;
+        const float shift = mx == -INFINITY ? 0.0f : mx;
+        const bool tiny = !SOFTMAX && mx < kTinyScore;
         // s, or up to a factor: e^{l - max} for a softmax and below kTinyScore
+        float s[VPL], z = 0.0f;
+        if (SOFTMAX || tiny) {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            if (p.softmax || tiny)
-                s[i] = l[i] == -INFINITY ? 0.0f : expf(l[i] - mx);
-            else
+            for (int i = 0; i < VPL; ++i) {
+                s[i] = expf(l[i] - shift);
+                z += s[i];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
                 s[i] = __fdividef(1.0f, 1.0f + expf(-l[i]));
-            z += s[i];
+                z += s[i];
+            }
         }
-        z = warp_sum(z);
-        const float rz = z > 0.0f ? __frcp_rn(z) : 0.0f;
+        float rz = 0.0f;
+        if (SOFTMAX || p.want_p) {
+            z = warp_sum(z);
+            rz = z > 0.0f ? __fdividef(1.0f, z) : 0.0f;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            const float q = s[i] * rz;
-            part[i] += q;
-            if (p.softmax)
-                s[i] = q;
+            for (int i = 0; i < VPL; ++i) {
+                const float q = s[i] * rz;
+                part[i] += q;
+                if (SOFTMAX)
+                    s[i] = q;
+            }
         }
         if (++held == 32) {          // 32-bit sums of 32 tokens, then 64
             held = 0;
@@ -407,125 +514,64 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
                 part[i] = 0.0f;
             }
         }
-        int mine = 0;
-        bool exact = near_matters && (tiny || p.group_top > 4);
-        if (!exact) {
-            uint32_t key[VPL];
-            float v[VPL];
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                const bool off = l[i] == -INFINITY || b[i] == -INFINITY;
-                v[i] = off ? -INFINITY : s[i] + b[i];
-                key[i] = e0 + i >= N ? 0u : (off ? 1u : order_key(p.bias ? v[i] : l[i]));
-            }
-            if (nodes) {
-                const float *s_node = nullptr;
-                float *sv = reinterpret_cast<float *>(s_val[warp]);
-                int count = 0;
-                const int g = lane / nl;
-                if (!p.node_direct) {
-#pragma unroll
-                    for (int i = 0; i < VPL; ++i)
-                        sv[e0 + i] = v[i];
-                    __syncwarp();
-                    s_node = sv + (g < p.n_groups ? g * per + lane % nl : 0);
-                    count = g < p.n_groups ? (per - lane % nl + nl - 1) / nl : 0;
-                }
-                const float sum = p.group_top <= 2
-                                      ? node_sum<2, VPL>(v, s_node, count, nl, p.group_top)
-                                      : node_sum<4, VPL>(v, s_node, count, nl, p.group_top);
-                uint32_t gkey = g < p.n_groups && lane % nl == 0 ? order_key(sum) : 0u;
-                uint32_t chosen = 0, m = 0;
-                for (int r = 0; r < p.topk_groups; ++r) {
-                    m = __reduce_max_sync(kAll, gkey);
-                    const int src = __ffs(__ballot_sync(kAll, gkey == m)) - 1;
-                    chosen |= 1u << (src / nl);
-                    if (lane == src)
-                        gkey = 0;
-                }
-                const uint32_t next = __reduce_max_sync(kAll, gkey);
-                exact = !(key_value(m) - key_value(next) > 4.0f * margin);
-#pragma unroll
-                for (int i = 0; i < VPL; ++i)
-                    if (e0 + i < N && !((chosen >> ((e0 + i) / per)) & 1u))
-                        key[i] = 0;
-                __syncwarp();
-            }
-            // the best of each lane; the winner's lane looks again
-            uint32_t best = 0;
-            int bi = 0;
+        int mine;
+        uint32_t won;
+        float le = -INFINITY;
+        if (!values) {
+            // the keys are the logits: exact, and the slot's logit is its key
 #pragma unroll
             for (int i = 0; i < VPL; ++i)
-                if (key[i] > best) {
-                    best = key[i];
-                    bi = i;
-                }
-            uint32_t my_key = 0;
-            const int rounds = p.bias && k < N ? k + 1 : k;
-            for (int j = 0; j < rounds; ++j) {
-                const uint32_t m = __reduce_max_sync(kAll, best);
-                const int src = __ffs(__ballot_sync(kAll, best == m)) - 1;
-                const int e = __shfl_sync(kAll, e0 + bi, src);
-                if (lane == j) {
-                    mine = e;
-                    my_key = m;
-                }
-                if (lane == src) {
-                    best = 0;
-                    const int gone = bi;
+                s[i] = l[i];
+            choose<float, uint32_t, VPL>(p, s, l, nullptr, 0.0f, k, mine, won);
+            if (lane < k && won > 1u)
+                le = key_value(won);
+        } else {
+            bool exact = tiny;
+            if (!exact) {
 #pragma unroll
-                    for (int i = 0; i < VPL; ++i) {
-                        if (i == gone)
-                            key[i] = 0;
-                        if (key[i] > best) {
-                            best = key[i];
-                            bi = i;
-                        }
-                    }
+                for (int i = 0; i < VPL; ++i)
+                    s[i] = l[i] == -INFINITY ? -INFINITY : s[i] + b[i];
+                // the sums of up to group_top values are off by that many times as much
+                exact = choose<float, uint32_t, VPL>(p, s, l, reinterpret_cast<float *>(s_val[warp]),
+                                                     margin * static_cast<float>(p.group_top),
+                                                     p.bias && k < N ? k + 1 : k, mine, won);
+                if (p.bias && !exact) {
+                    // each slot against the next one, the last against the first left out
+                    const uint32_t nk = __shfl_down_sync(kAll, won, 1);
+                    const int ne = __shfl_down_sync(kAll, mine, 1);
+                    bool close = lane < k && nk > 1u && !(key_value(won) - key_value(nk) > margin);
+                    if (close)
+                        // equal logits with equal biases are equal in every precision
+                        close = won != nk || load_logit<BF16>(row, mine) != load_logit<BF16>(row, ne) ||
+                                p.bias[mine] != p.bias[ne];
+                    exact = __any_sync(kAll, close);
                 }
             }
-            if (p.bias && !exact) {
-                // each slot against the next one, the last against the first left out
-                const uint32_t nk = __shfl_down_sync(kAll, my_key, 1);
-                const int ne = __shfl_down_sync(kAll, mine, 1);
-                bool close = false;
-                if (lane < k && nk > 1u && !(key_value(my_key) - key_value(nk) > 2.0f * margin)) {
-                    // equal logits with equal biases are equal in every precision
-                    const bool same =
-                        load_logit<BF16>(row, mine) == load_logit<BF16>(row, ne) &&
-                        (!p.bias || p.bias[mine] == p.bias[ne]);
-                    close = !same || my_key != nk;
-                }
-                exact = __any_sync(kAll, close);
-            }
+            if (exact)
+                mine = choose_exact<VPL, BF16, SOFTMAX>(p, row, s_val[warp]);
+            bool ignore = false;
+            if (lane < k)
+                le = clean_logit(load_logit<BF16>(row, mine), ignore);
         }
-        if (exact)
-            mine = choose_exact<VPL, BF16>(p, row, s_val[warp]);
         // weights: lane j has expert e_j; renormalised ones up to a common factor
-        bool ignore = false;
-        const float le = lane < k ? clean_logit(load_logit<BF16>(row, mine), ignore) : -INFINITY;
-        const float mc = p.renorm ? slot_max(le) : mx;
-        float w = 0.0f;
-        if (le != -INFINITY) {
-            if (p.softmax)
-                w = expf(le - mc) * (p.renorm ? 1.0f : rz);
-            else if (p.renorm && mc < kTinyScore)
-                w = expf(le - mc);
-            else
-                w = 1.0f / (1.0f + expf(-le));
-        }
+        const float mc = p.renorm ? slot_max(le) : shift;
+        float w;
+        if (SOFTMAX || (p.renorm && mc < kTinyScore))
+            w = expf(le - (mc == -INFINITY ? 0.0f : mc)) * (p.renorm ? 1.0f : rz);
+        else
+            w = __fdividef(1.0f, 1.0f + expf(-le));
         if (p.renorm) {
             const float d = slot_sum(w);
-            w = d > 0.0f ? w / d : 0.0f;
+            w = d > 0.0f ? __fdividef(w, d) : 0.0f;
         }
         if (lane < k) {
-            p.topk_idx[t * k + lane] = mine;
-            p.topk_w[t * k + lane] = w * p.scale;
+            p.topk_idx[slot] = mine;
+            p.topk_w[slot] = w * p.scale;
         }
     }
     if (bad)
         set_status(p.status, DEV_NAN_LOGIT);
-    if (p.p_part || p.p_mean) {
+    if (p.want_p) {
         // the block's sums, warp by warp in order
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
@@ -612,8 +658,9 @@ __device__ __forceinline__ void logistic(float l, float &s, float &om)
 // not underflow.  One warp per token: the logits are read once and the
 // gradient is written once (2 T N values, the bound by bytes), the k chosen
 // experts' gradients a second time by the lanes that hold the slots.
-template <int VPL, bool BF16>
-__global__ void __launch_bounds__(kThreads) route_grad_kernel(const __grid_constant__ RouteGradParams p)
+template <int VPL, bool BF16, bool SOFTMAX>
+__global__ void __launch_bounds__(kThreads, 4)
+    route_grad_kernel(const __grid_constant__ RouteGradParams p)
 {
     grid_dep_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -624,35 +671,36 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(const __grid_const
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
         c[i] = (p.dp_mean && e0 + i < N) ? p.dp_mean[e0 + i] * inv_t : 0.0f;
-    const int64_t esz = BF16 ? 2 : 4;
-    const int64_t nwarps = static_cast<int64_t>(gridDim.x) * kWarps;
     bool bad = false, nan = false;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
+    const int64_t row_bytes = p.ld * (BF16 ? 2 : 4);
+    const int64_t row_step = step * row_bytes;
     int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    const uint8_t *row = static_cast<const uint8_t *>(p.logits) + t * row_bytes;
+    uint8_t *out = static_cast<uint8_t *>(p.dlogits) + t * row_bytes;
+    const int64_t slot_step = step * k;
+    int64_t slot = t * k + lane;
+    const bool slots = p.dtopk_w != nullptr && lane < k;
     float nxt[VPL];
     int nme = -1;
     float ng = 0.0f;
-    auto fetch = [&](int64_t at) {
-        load_logits<VPL, BF16>(static_cast<const uint8_t *>(p.logits) + at * p.ld * esz, e0, N,
-                               p.vec, nxt);
-        if (lane < k && p.dtopk_w) {
-            nme = p.topk_idx[at * k + lane];
-            ng = p.dtopk_w[at * k + lane];
+    if (t < p.T) {
+        load_logits<VPL, BF16>(row, e0, N, p.vec, nxt);
+        if (slots) {
+            nme = p.topk_idx[slot];
+            ng = p.dtopk_w[slot];
         }
-    };
-    if (t < p.T)
-        fetch(t);
-    for (; t < p.T; t += nwarps) {
-        const void *row = static_cast<const uint8_t *>(p.logits) + t * p.ld * esz;
-        void *out = static_cast<uint8_t *>(p.dlogits) + t * p.ld * esz;
+    }
+    for (; t < p.T; t += step, row += row_step, out += row_step) {
         // chosen slots, one per lane
-        int me = -1;
+        int me = nme;
         float lc = -INFINITY, cm = 0.0f;
         const float g = p.scale * ng;
-        if (lane < k && p.dtopk_w) {
-            if (nme < 0 || nme >= N) {
+        if (slots) {
+            if (static_cast<uint32_t>(me) >= static_cast<uint32_t>(N)) {
                 bad = true;
+                me = -1;
             } else {
-                me = nme;
                 lc = clean_logit(load_logit<BF16>(row, me), nan);
                 if (p.dp_mean)
                     cm = p.dp_mean[me] * inv_t;
@@ -664,62 +712,74 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(const __grid_const
             l[i] = clean_logit(nxt[i], nan);
             mx = fmaxf(mx, l[i]);
         }
-        if (t + nwarps < p.T)
-            fetch(t + nwarps);
-        // the shift of the exponentials: none for the logistic function unless it is tiny
-        const bool tiny = !p.softmax && warp_max(mx) < kTinyScore;
-        mx = (p.softmax || tiny) ? warp_max(mx) : 0.0f;
-        float s[VPL], om[VPL], z = 0.0f, cz = 0.0f;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            om[i] = 1.0f;
-            if (p.softmax || tiny)
-                s[i] = l[i] == -INFINITY ? 0.0f : expf(l[i] - mx);
-            else
-                logistic(l[i], s[i], om[i]);
-            z += s[i];
-            cz = fmaf(c[i], s[i], cz);
+        slot += slot_step;
+        if (t + step < p.T) {
+            load_logits<VPL, BF16>(row + row_step, e0, N, p.vec, nxt);
+            if (slots) {
+                nme = p.topk_idx[slot];
+                ng = p.dtopk_w[slot];
+            }
         }
-        z = warp_sum(z);
-        if (p.dp_mean)
+        mx = warp_max(mx);
+        // the shift of the exponentials: none for the logistic function unless it is tiny
+        const bool tiny = !SOFTMAX && mx < kTinyScore;
+        const float shift = mx == -INFINITY ? 0.0f : mx;
+        float s[VPL], om[VPL], z = 0.0f, cz = 0.0f;
+        if (SOFTMAX || tiny) {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                om[i] = 1.0f;
+                s[i] = expf(l[i] - shift);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                logistic(l[i], s[i], om[i]);
+        }
+        float rz = 0.0f;
+        if (SOFTMAX || p.dp_mean) {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                z += s[i];
+                cz = fmaf(c[i], s[i], cz);
+            }
+            z = warp_sum(z);
             cz = warp_sum(cz);
-        const float rz = z > 0.0f ? __frcp_rn(z) : 0.0f;
+            rz = z > 0.0f ? __fdividef(1.0f, z) : 0.0f;
+        }
         const float cq = cz * rz;
         // chosen: score (up to a factor when renormalised), 1 - s, share of the row's sum
-        float sc = 0.0f, oc = 1.0f, share = 0.0f;
-        const float mc = p.renorm ? slot_max(lc) : mx;
-        if (lc != -INFINITY) {
-            if (p.softmax || (p.renorm && mc < kTinyScore))
-                sc = expf(lc - mc) * (p.renorm ? 1.0f : rz);
-            else
-                logistic(lc, sc, oc);
-            if (p.softmax || tiny) {
-                share = expf(lc - mx) * rz;
-            } else {
-                float so;
-                logistic(lc, so, oc);
-                share = so * rz;
-            }
+        float sc, oc, share;
+        if (SOFTMAX) {
+            oc = 1.0f;
+            share = expf(lc - shift) * rz;
+            sc = share;
+        } else {
+            logistic(lc, sc, oc);
+            share = (tiny ? expf(lc - shift) : sc) * rz;
         }
         float u, gp = 0.0f;
         if (p.renorm) {
+            const float mc = slot_max(lc);
+            if (SOFTMAX || mc < kTinyScore)
+                sc = expf(lc - (mc == -INFINITY ? 0.0f : mc));
             const float d = slot_sum(sc);
             const float r = d > 0.0f ? __fdividef(sc, d) : 0.0f;
             u = r * (g - slot_sum(r * g));
         } else {
             u = sc * g;
-            if (p.softmax)
+            if (SOFTMAX)
                 gp = __shfl_sync(kAll, slot_sum(u), 0);
         }
         // the same expert in several slots adds up
-        float us = 0.0f;
-        if (p.dtopk_w) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int ej = __shfl_sync(kAll, me, j);
+        const unsigned twins = __match_any_sync(kAll, me >= 0 ? me : -1 - lane);
+        if (__any_sync(kAll, (twins & (twins - 1)) != 0u)) {
+            float us = 0.0f;
+            for (int j = 0; j < k; ++j) {
                 const float uj = __shfl_sync(kAll, u, j);
-                us += ej == me ? uj : 0.0f;
+                us += (twins >> j) & 1u ? uj : 0.0f;
             }
+            u = us;
         }
         // every expert without its slots' share, then the chosen ones with it
         const float sub = cq + gp;
@@ -730,7 +790,7 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(const __grid_const
         store_logits<VPL, BF16>(out, e0, N, p.vec, d);
         __syncwarp();
         if (me >= 0)
-            store_logit<BF16>(out, me, lc == -INFINITY ? 0.0f : oc * (share * (cm - sub) + us));
+            store_logit<BF16>(out, me, lc == -INFINITY ? 0.0f : oc * (share * (cm - sub) + u));
     }
     if (bad)
         set_status(p.status, DEV_BAD_EXPERT);
@@ -738,13 +798,14 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(const __grid_const
         set_status(p.status, DEV_NAN_LOGIT);
 }
 
-int route_grid(int64_t T)
+// As many blocks as there is work for, at most those that run at once.
+int route_grid(int64_t T, int per_sm)
 {
     int sms = 148, dev = 0;
     if (cudaGetDevice(&dev) == cudaSuccess)
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     int64_t g = (T + kWarps - 1) / kWarps;
-    int64_t cap = static_cast<int64_t>(sms) * 4;
+    int64_t cap = static_cast<int64_t>(sms) * per_sm;
     if (cap > kRouteMaxBlocks)
         cap = kRouteMaxBlocks;
     return static_cast<int>(g < cap ? g : cap);
@@ -798,8 +859,9 @@ cudaError_t launch_route(const RouteLaunch &L, cudaStream_t stream)
         // a node's values lie on whole lanes, a power of two of them, or are
         // gathered onto 32 / n_groups lanes
         const int v = lane_values(L.N), per = L.N / L.n_groups;
+        p.per_node = per;
         const int lanes = per / v;
-        if (per % v == 0 && (lanes & (lanes - 1)) == 0) {
+        if (per % v == 0 && (lanes & (lanes - 1)) == 0 && L.group_top <= 4) {
             p.node_lanes = lanes;
             p.node_direct = 1;
         } else {
@@ -809,16 +871,17 @@ cudaError_t launch_route(const RouteLaunch &L, cudaStream_t stream)
             p.node_lanes = lg;
         }
     }
-    const int grid = route_grid(L.T);
+    const int grid = route_grid(L.T, lane_values(L.N) == 8 ? 3 : 4);
+    p.want_p = L.p_mean != nullptr;
     // one block writes its sums as the result
     p.p_mean = grid == 1 ? L.p_mean : nullptr;
     p.p_part = L.p_mean && grid > 1 ? L.p_part : nullptr;
     with_vpl(L.N, [&](auto v) {
         constexpr int VPL = decltype(v)::value;
-        if (L.dtype == MOE_BF16)
-            launch_k(route_kernel<VPL, true>, grid, kThreads, 0, stream, p);
-        else
-            launch_k(route_kernel<VPL, false>, grid, kThreads, 0, stream, p);
+        auto kernel = L.dtype == MOE_BF16
+                          ? (p.softmax ? route_kernel<VPL, true, true> : route_kernel<VPL, true, false>)
+                          : (p.softmax ? route_kernel<VPL, false, true> : route_kernel<VPL, false, false>);
+        launch_k(kernel, grid, kThreads, 0, stream, p);
     });
     count_launches(1);
     const cudaError_t e = cudaGetLastError();
@@ -844,13 +907,13 @@ cudaError_t launch_route_grad(const RouteGradLaunch &L, cudaStream_t stream)
     p.scale = L.scale;
     p.status = L.status;
     p.vec = rows_on_16(L.logits, L.ld, L.dtype) && rows_on_16(L.dlogits, L.ld, L.dtype);
-    const int grid = route_grid(L.T);
+    const int grid = route_grid(L.T, 4);
     with_vpl(L.N, [&](auto v) {
         constexpr int VPL = decltype(v)::value;
-        if (L.dtype == MOE_BF16)
-            launch_k(route_grad_kernel<VPL, true>, grid, kThreads, 0, stream, p);
-        else
-            launch_k(route_grad_kernel<VPL, false>, grid, kThreads, 0, stream, p);
+        auto kernel = L.dtype == MOE_BF16
+                          ? (p.softmax ? route_grad_kernel<VPL, true, true> : route_grad_kernel<VPL, true, false>)
+                          : (p.softmax ? route_grad_kernel<VPL, false, true> : route_grad_kernel<VPL, false, false>);
+        launch_k(kernel, grid, kThreads, 0, stream, p);
     });
     count_launches(1);
     return cudaGetLastError();
