@@ -158,25 +158,52 @@ def test_linear_argument_refusals(lib):
     assert back(ws=None) == wsp and back(ws=P(FAKE + 8)) == wsp and back(n=nb_ - 1) == wsp
 
 
+class OnDevice:
+    """A host tensor that answers as one on cuda:0 would: the binding's own checks come before
+    anything is launched, so they can be seen without a GPU."""
+
+    def __init__(self, t, index=0):
+        self._t, self._index = t, index
+
+    def __getattr__(self, name):
+        return getattr(self._t, name)
+
+    is_cuda = True
+
+    def get_device(self):
+        return self._index
+
+
 def test_binding_refuses_wrong_tensors(lib):
     """Element type, shape, strides and device are checked where the C call sees addresses only."""
     cfg = moe.make_route_config(4, 8, 2)
-    ws = torch.zeros(moe.moe_route_workspace_bytes(cfg), dtype=torch.uint8)
+    ws = OnDevice(torch.zeros(moe.moe_route_workspace_bytes(cfg), dtype=torch.uint8))
     l, idx, w = torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
     bad = [(l.double(), None, idx, w), (l[:3], None, idx, w), (torch.zeros(8, 4).t(), None, idx, w),
            (torch.zeros(4, 16)[:, ::2], None, idx, w), (torch.zeros(4, 9)[:, :8], None, idx, w),
            (l, torch.zeros(7), idx, w), (l, None, idx.long(), w), (l, None, idx, w.half()),
-           (None, None, idx, w), (l, None, None, w)]
+           (l, None, torch.zeros(2, 4, dtype=torch.int32).t(), w), (None, None, idx, w),
+           (l, None, None, w)]
     for args in bad:
         with pytest.raises(moe.MoeError) as err:
-            moe.moe_route(cfg, *args, None, ws)
+            moe.moe_route(cfg, *[None if a is None else OnDevice(a) for a in args], None, ws)
         assert err.value.status == moe.MOE_ERR_INVALID_ARG
-    with pytest.raises(moe.MoeError) as err:                  # a workspace on the host
-        moe.moe_route(cfg, l, None, idx, w, None, ws)
-    assert err.value.status == moe.MOE_ERR_WORKSPACE
+    with pytest.raises(moe.MoeError) as err:                  # on another device than the workspace
+        moe.moe_route(cfg, OnDevice(l, 1), None, OnDevice(idx), OnDevice(w), None, ws)
+    assert err.value.status == moe.MOE_ERR_INVALID_ARG
+    for other in (ws._t, OnDevice(ws._t[::2])):               # a workspace on the host, or with gaps
+        with pytest.raises(moe.MoeError) as err:
+            moe.moe_route(cfg, OnDevice(l), None, OnDevice(idx), OnDevice(w), None, other)
+        assert err.value.status == moe.MOE_ERR_WORKSPACE
+    padded = moe.make_route_config(4, 8, 2, ld=9)
+    with pytest.raises(moe.MoeError):                         # gaps announced, but not there
+        moe.moe_route(padded, OnDevice(l), None, OnDevice(idx), OnDevice(w), None, ws)
     lc = moe.make_linear_config(4, 8, 3)
-    with pytest.raises(moe.MoeError):
-        moe.moe_linear(lc, torch.zeros(4, 8), torch.zeros(3, 8), None, None, torch.zeros(4, 3), None, ws)
+    x, W, y = torch.zeros(4, 8).bfloat16(), torch.zeros(3, 8).bfloat16(), torch.zeros(4, 3).bfloat16()
+    for args in ((x.float(), W, y), (x, W.t().contiguous(), y), (x, W, y.float())):
+        a = [OnDevice(t) for t in args]
+        with pytest.raises(moe.MoeError):
+            moe.moe_linear(lc, a[0], a[1], None, None, a[2], None, ws)
     with pytest.raises(moe.MoeError):
         moe.route_workspace(moe.make_route_config(4, 8, 9))
     with pytest.raises(moe.MoeError):

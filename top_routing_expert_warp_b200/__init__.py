@@ -327,15 +327,31 @@ def workspace(cfg: moe_config, device="cuda"):
 
 
 # ------------------------------------------------------------------ the gate and the projections
-_TORCH_DTYPES = {}
+# torch, its element types by code, and its raw queries of the current device and stream: bound at
+# the first call (they cost a fraction of the public ones, and a small call is bound by the host).
+_t = None
 
 
-def _torch_dtype(code):
-    if not _TORCH_DTYPES:
+class _Torch:
+    def __init__(self):
         import torch
-        _TORCH_DTYPES.update({MOE_F32: torch.float32, MOE_BF16: torch.bfloat16,
-                              "i32": torch.int32})
-    return _TORCH_DTYPES[code]
+        self.dtype = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16, "i32": torch.int32}
+        self.device_guard = torch.cuda.device
+        c = torch._C
+        self.current_device = getattr(c, "_cuda_getDevice", None) or torch.cuda.current_device
+        self.raw_stream = getattr(c, "_cuda_getCurrentRawStream", None) or (
+            lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
+def _enter(where, workspace):
+    """Device index of the workspace."""
+    global _t
+    if _t is None:
+        _t = _Torch()
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise MoeError(MOE_ERR_WORKSPACE,
+                       f"{where}: the workspace is on {workspace.device} or not contiguous")
+    return workspace.get_device()
 
 
 def _arg(where, device, name, t, code, shape, ld=None, optional=False):
@@ -345,42 +361,37 @@ def _arg(where, device, name, t, code, shape, ld=None, optional=False):
         if optional:
             return None
         raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: {name} is missing")
-    if isinstance(t, int):
+    if type(t) is int:
         return t
-    if t.dtype is not _torch_dtype(code):
+    if t.dtype is not _t.dtype[code]:
         raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: {name} is {t.dtype}")
     if t.shape != shape:
         raise MoeError(MOE_ERR_INVALID_ARG,
                        f"{where}: {name} is {list(t.shape)}, not {list(shape)}")
-    if ld is None:
-        if not t.is_contiguous():
+    without_gaps = ld is None or ld == shape[1]
+    if not (without_gaps and t.is_contiguous()):
+        if ld is None:
             raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: {name} is not contiguous")
-    else:
         s0, s1 = t.stride()
         if (s1 != 1 and shape[1] > 1) or (s0 != ld and shape[0] > 1):
             raise MoeError(MOE_ERR_INVALID_ARG,
                            f"{where}: {name} has strides {(s0, s1)}, not {(ld, 1)}")
-    if t.device != device:
+    if t.get_device() != device:
         raise MoeError(MOE_ERR_INVALID_ARG,
-                       f"{where}: {name} is on {t.device}, the workspace on {device}")
+                       f"{where}: {name} is on {t.device}, the workspace on cuda:{device}")
     return t.data_ptr()
 
 
-def _call(where, fn, workspace, stream, *args):
+def _call(where, fn, device, workspace, stream, *args):
     """Runs a C entry point with the workspace's device current (on ``stream``, or that
     device's current stream)."""
-    import torch
-    dev = workspace.device
-    if dev.type != "cuda":
-        raise MoeError(MOE_ERR_WORKSPACE, f"{where}: the workspace is on {dev}")
     nbytes = workspace.numel() * workspace.element_size()
-    if not workspace.is_contiguous():
-        raise MoeError(MOE_ERR_WORKSPACE, f"{where}: the workspace is not contiguous")
-    if dev.index == torch.cuda.current_device():
-        status = fn(*args, workspace.data_ptr(), nbytes, _stream(stream))
+    s = _t.raw_stream(device) if stream is None else _stream(stream)
+    if device == _t.current_device():
+        status = fn(*args, workspace.data_ptr(), nbytes, s)
     else:
-        with torch.cuda.device(dev):
-            status = fn(*args, workspace.data_ptr(), nbytes, _stream(stream))
+        with _t.device_guard(device):
+            status = fn(*args, workspace.data_ptr(), nbytes, s)
     if status != MOE_OK:
         raise MoeError(status, where)
 
@@ -411,9 +422,10 @@ def _zeros(nbytes, where, device):
 
 
 def moe_route(cfg, logits, bias, topk_idx, topk_w, p_mean, workspace, stream=None):
-    a, dev = "moe_route", workspace.device
+    a = "moe_route"
+    dev = _enter(a, workspace)
     T, N, k = cfg.T, cfg.N, cfg.k
-    _call(a, lib().moe_route, workspace, stream, ctypes.byref(cfg),
+    _call(a, lib().moe_route, dev, workspace, stream, ctypes.byref(cfg),
           _arg(a, dev, "logits", logits, cfg.dtype, (T, N), cfg.ld),
           _arg(a, dev, "bias", bias, MOE_F32, (N,), optional=True),
           _arg(a, dev, "topk_idx", topk_idx, "i32", (T, k)),
@@ -422,9 +434,10 @@ def moe_route(cfg, logits, bias, topk_idx, topk_w, p_mean, workspace, stream=Non
 
 
 def moe_route_backward(cfg, logits, topk_idx, dtopk_w, dp_mean, dlogits, workspace, stream=None):
-    a, dev = "moe_route_backward", workspace.device
+    a = "moe_route_backward"
+    dev = _enter(a, workspace)
     T, N, k = cfg.T, cfg.N, cfg.k
-    _call(a, lib().moe_route_backward, workspace, stream, ctypes.byref(cfg),
+    _call(a, lib().moe_route_backward, dev, workspace, stream, ctypes.byref(cfg),
           _arg(a, dev, "logits", logits, cfg.dtype, (T, N), cfg.ld),
           _arg(a, dev, "topk_idx", topk_idx, "i32", (T, k), optional=dtopk_w is None),
           _arg(a, dev, "dtopk_w", dtopk_w, MOE_F32, (T, k), optional=True),
@@ -434,10 +447,11 @@ def moe_route_backward(cfg, logits, topk_idx, dtopk_w, dp_mean, dlogits, workspa
 
 def moe_combine_backward(cfg, dy, y_perm, inv_row, topk_w, dy_perm, dtopk_w, workspace,
                          stream=None):
-    a, dev = "moe_combine_backward", workspace.device
+    a = "moe_combine_backward"
+    dev = _enter(a, workspace)
     T, d, k = cfg.T, cfg.d, cfg.k
     rows = T * k
-    _call(a, lib().moe_combine_backward, workspace, stream, ctypes.byref(cfg),
+    _call(a, lib().moe_combine_backward, dev, workspace, stream, ctypes.byref(cfg),
           _arg(a, dev, "dy", dy, cfg.dtype, (T, d)),
           _arg(a, dev, "y_perm", y_perm, cfg.dtype, (rows, d), optional=dtopk_w is None),
           _arg(a, dev, "inv_row", inv_row, "i32", (rows,)),
@@ -467,9 +481,10 @@ def linear_workspace(cfg: moe_linear_config, device="cuda", backward=True):
 
 
 def moe_linear(cfg, x, W, bias, residual, y, preact, workspace, stream=None):
-    a, dev = "moe_linear", workspace.device
+    a = "moe_linear"
+    dev = _enter(a, workspace)
     M, K, N = cfg.M, cfg.n_in, cfg.n_out
-    _call(a, lib().moe_linear, workspace, stream, ctypes.byref(cfg),
+    _call(a, lib().moe_linear, dev, workspace, stream, ctypes.byref(cfg),
           _arg(a, dev, "x", x, cfg.dtype, (M, K), cfg.ldx),
           _arg(a, dev, "W", W, cfg.dtype, (N, K)),
           _arg(a, dev, "bias", bias, MOE_F32, (N,), optional=True),
@@ -479,9 +494,10 @@ def moe_linear(cfg, x, W, bias, residual, y, preact, workspace, stream=None):
 
 
 def moe_linear_backward(cfg, dy, x, W, preact, dx, dW, db, workspace, stream=None):
-    a, dev = "moe_linear_backward", workspace.device
+    a = "moe_linear_backward"
+    dev = _enter(a, workspace)
     M, K, N = cfg.M, cfg.n_in, cfg.n_out
-    _call(a, lib().moe_linear_backward, workspace, stream, ctypes.byref(cfg),
+    _call(a, lib().moe_linear_backward, dev, workspace, stream, ctypes.byref(cfg),
           _arg(a, dev, "dy", dy, cfg.out_dtype, (M, N), cfg.ldy),
           _arg(a, dev, "x", x, cfg.dtype, (M, K), cfg.ldx, optional=dW is None),
           _arg(a, dev, "W", W, cfg.dtype, (N, K), optional=dx is None),

@@ -3,9 +3,10 @@
 //   y[t] = sum over kept slots j of w[t, j] * y_perm[r(t, j)]
 //   dy_perm[r(t, j)] = w[t, j] * dy[t],   dw[t, j] = <dy[t], y_perm[r(t, j)]>
 //
-// One block per token: each thread reads its chunks of dy[t] once and uses
-// them for every slot.  fp32 products and sums, the order of a sum fixed by
-// the block's shape.
+// Each lane reads its chunks of dy[t] once and uses them for every slot; the
+// loads of all slots of a pass are issued before any is used.  fp32 products
+// and sums, the order of a sum fixed by the thread count.  Bound by bytes: dy
+// and the kept rows of y_perm read once, those of dy_perm written once.
 #include "common.cuh"
 #include "kernels.h"
 #include "moe.h"
@@ -17,7 +18,24 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxK = 8;
 
-template <bool BF16>
+template <bool BF16, int V>
+__device__ __forceinline__ void unpack(const uint4 q, float (&v)[V])
+{
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (BF16) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        } else {
+            v[i] = __uint_as_float(w[i]);
+        }
+    }
+}
+
+// KM: bound on k.  TPT threads per token: a warp, or the block for batches too
+// small to fill the GPU with warps.  DW, DY: which outputs are wanted.
+template <bool BF16, int KM, int TPT, bool DW, bool DY>
 __global__ void __launch_bounds__(kThreads)
     combine_grad_kernel(const uint8_t *__restrict__ dy, const uint8_t *y_perm,
                         const int32_t *__restrict__ inv_row, const float *__restrict__ topk_w,
@@ -25,94 +43,163 @@ __global__ void __launch_bounds__(kThreads)
                         int64_t rows_cap, uint32_t *status)
 {
     grid_dep_wait();
-    __shared__ float s_dot[kMaxK][kThreads / 32];
+    __shared__ float s_dot[kThreads / 32][KM];
     constexpr int V = BF16 ? 8 : 4;
     constexpr int esz = BF16 ? 2 : 4;
+    constexpr int U = KM <= 2 ? 4 : (KM <= 4 ? 2 : 1);   // chunks per thread and pass
+    constexpr int TPB = kThreads / TPT;                  // tokens per block
     const int chunks = d / V;
+    const int64_t row_bytes = static_cast<int64_t>(d) * esz;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
-        int32_t row[kMaxK];
-        float w[kMaxK], dot[kMaxK];
-#pragma unroll
-        for (int j = 0; j < kMaxK; ++j) {
-            row[j] = j < k ? inv_row[t * k + j] : -1;
-            if (row[j] >= rows_cap || row[j] < -1) {
-                if (threadIdx.x == 0)
-                    set_status(status, DEV_BAD_ROW);
-                row[j] = -1;
+    const int me = threadIdx.x % TPT;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * TPB + threadIdx.x / TPT; t < T;
+         t += static_cast<int64_t>(gridDim.x) * TPB) {
+        int32_t my_row = -1;
+        float my_w = 0.0f;
+        if (lane < k) {
+            my_row = inv_row[t * k + lane];
+            if (DY)
+                my_w = topk_w[t * k + lane];
+            if (my_row >= rows_cap || my_row < -1) {
+                set_status(status, DEV_BAD_ROW);
+                my_row = -1;
             }
-            w[j] = (j < k && dy_perm) ? topk_w[t * k + j] : 0.0f;
+        }
+        int32_t row[KM];
+        float w[KM], dot[KM];
+#pragma unroll
+        for (int j = 0; j < KM; ++j) {
+            row[j] = __shfl_sync(0xffffffffu, my_row, j);
+            w[j] = __shfl_sync(0xffffffffu, my_w, j);
             dot[j] = 0.0f;
         }
-        const uint4 *src = reinterpret_cast<const uint4 *>(dy + t * static_cast<int64_t>(d) * esz);
-        for (int c = threadIdx.x; c < chunks; c += kThreads) {
-            const uint4 a = src[c];
-            const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
-            float x[V];
+        const uint4 *src = reinterpret_cast<const uint4 *>(dy + t * row_bytes);
+        for (int c0 = me; c0 < chunks; c0 += TPT * U) {
+            uint4 a[U], y[DW ? KM : 1][U];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (BF16) {
-                    x[2 * i] = __uint_as_float(aw[i] << 16);
-                    x[2 * i + 1] = __uint_as_float(aw[i] & 0xFFFF0000u);
-                } else {
-                    x[i] = __uint_as_float(aw[i]);
-                }
+            for (int u = 0; u < U; ++u)
+                a[u] = c0 + TPT * u < chunks ? __ldg(src + c0 + TPT * u) : make_uint4(0, 0, 0, 0);
+            if (DW) {
+#pragma unroll
+                for (int j = 0; j < KM; ++j)
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        y[DW ? j : 0][u] =
+                            (row[j] >= 0 && c0 + TPT * u < chunks)
+                                ? reinterpret_cast<const uint4 *>(y_perm + row[j] * row_bytes)[c0 + TPT * u]
+                                : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
-            for (int j = 0; j < kMaxK; ++j) {
-                if (row[j] < 0)
-                    continue;
-                const int64_t off = static_cast<int64_t>(row[j]) * d * esz;
-                if (dtopk_w) {
-                    const uint4 v = reinterpret_cast<const uint4 *>(y_perm + off)[c];
-                    const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+            for (int u = 0; u < U; ++u) {
+                const int c = c0 + TPT * u;
+                float x[V];
+                unpack<BF16, V>(a[u], x);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (BF16) {
-                            dot[j] = fmaf(x[2 * i], __uint_as_float(vw[i] << 16), dot[j]);
-                            dot[j] = fmaf(x[2 * i + 1], __uint_as_float(vw[i] & 0xFFFF0000u), dot[j]);
-                        } else {
-                            dot[j] = fmaf(x[i], __uint_as_float(vw[i]), dot[j]);
+                for (int j = 0; j < KM; ++j) {
+                    if (DW) {
+                        float v[V];
+                        unpack<BF16, V>(y[DW ? j : 0][u], v);
+                        if (row[j] >= 0) {       // a dropped slot adds nothing, whatever dy holds
+#pragma unroll
+                            for (int i = 0; i < V; ++i)
+                                dot[j] = fmaf(x[i], v[i], dot[j]);
                         }
                     }
-                }
-                if (dy_perm) {
-                    uint4 o;
-                    if (BF16) {
-                        o.x = pack_bf16x2(w[j] * x[0], w[j] * x[1]);
-                        o.y = pack_bf16x2(w[j] * x[2], w[j] * x[3]);
-                        o.z = pack_bf16x2(w[j] * x[V - 4], w[j] * x[V - 3]);
-                        o.w = pack_bf16x2(w[j] * x[V - 2], w[j] * x[V - 1]);
-                    } else {
-                        o.x = __float_as_uint(w[j] * x[0]);
-                        o.y = __float_as_uint(w[j] * x[1]);
-                        o.z = __float_as_uint(w[j] * x[2]);
-                        o.w = __float_as_uint(w[j] * x[3]);
+                    if (DY && row[j] >= 0 && c < chunks) {
+                        uint4 o;
+                        if (BF16) {
+                            o.x = pack_bf16x2(w[j] * x[0], w[j] * x[1]);
+                            o.y = pack_bf16x2(w[j] * x[2], w[j] * x[3]);
+                            o.z = pack_bf16x2(w[j] * x[V - 4], w[j] * x[V - 3]);
+                            o.w = pack_bf16x2(w[j] * x[V - 2], w[j] * x[V - 1]);
+                        } else {
+                            o.x = __float_as_uint(w[j] * x[0]);
+                            o.y = __float_as_uint(w[j] * x[1]);
+                            o.z = __float_as_uint(w[j] * x[2]);
+                            o.w = __float_as_uint(w[j] * x[3]);
+                        }
+                        reinterpret_cast<uint4 *>(dy_perm + row[j] * row_bytes)[c] = o;
                     }
-                    reinterpret_cast<uint4 *>(dy_perm + off)[c] = o;
                 }
             }
         }
-        if (dtopk_w) {
+        if (DW) {
+            float mine = 0.0f;
 #pragma unroll
-            for (int j = 0; j < kMaxK; ++j) {
+            for (int j = 0; j < KM; ++j) {
                 float v = dot[j];
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1)
                     v += __shfl_xor_sync(0xffffffffu, v, o);
-                if (lane == 0)
-                    s_dot[j][warp] = v;
+                if (lane == j)
+                    mine = v;
             }
-            __syncthreads();
-            if (threadIdx.x < k) {
-                float v = 0.0f;
-                for (int i = 0; i < kThreads / 32; ++i)
-                    v += s_dot[threadIdx.x][i];
-                dtopk_w[t * k + threadIdx.x] = v;
+            if (TPT == 32) {
+                if (lane < k)
+                    dtopk_w[t * k + lane] = mine;
+            } else {
+                if (lane < KM)
+                    s_dot[warp][lane] = mine;
+                __syncthreads();
+                if (threadIdx.x < k) {
+                    float v = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < kThreads / 32; ++i)
+                        v += s_dot[i][threadIdx.x];
+                    dtopk_w[t * k + threadIdx.x] = v;
+                }
+                __syncthreads();
             }
-            __syncthreads();
         }
     }
+}
+
+struct Args {
+    const uint8_t *dy, *y_perm;
+    const int32_t *inv_row;
+    const float *topk_w;
+    uint8_t *dy_perm;
+    float *dtopk_w;
+    int64_t T;
+    int32_t d, k, sms;
+    uint32_t *status;
+    cudaStream_t stream;
+};
+
+template <bool BF16, int KM, int TPT>
+void run(const Args &a)
+{
+    constexpr int TPB = kThreads / TPT;
+    const int64_t want = (a.T + TPB - 1) / TPB, cap = static_cast<int64_t>(a.sms) * 8;
+    auto kernel = a.dtopk_w ? (a.dy_perm ? combine_grad_kernel<BF16, KM, TPT, true, true>
+                                         : combine_grad_kernel<BF16, KM, TPT, true, false>)
+                            : combine_grad_kernel<BF16, KM, TPT, false, true>;
+    launch_k(kernel, static_cast<int>(want < cap ? want : cap), kThreads, 0, a.stream, a.dy, a.y_perm,
+             a.inv_row, a.topk_w, a.dy_perm, a.dtopk_w, a.T, a.d, a.k, a.T * a.k, a.status);
+    count_launches(1);
+}
+
+template <bool BF16, int KM>
+void run_km(const Args &a)
+{
+    // a warp per token once there are more tokens than two blocks per SM
+    if (a.T > static_cast<int64_t>(a.sms) * 2)
+        run<BF16, KM, 32>(a);
+    else
+        run<BF16, KM, kThreads>(a);
+}
+
+template <bool BF16>
+void run_k(const Args &a)
+{
+    if (a.k <= 1)
+        run_km<BF16, 1>(a);
+    else if (a.k <= 2)
+        run_km<BF16, 2>(a);
+    else if (a.k <= 4)
+        run_km<BF16, 4>(a);
+    else
+        run_km<BF16, kMaxK>(a);
 }
 
 }  // namespace
@@ -127,14 +214,12 @@ cudaError_t launch_combine_grad(int dtype, const void *dy, const void *y_perm,
     int sms = 148, dev = 0;
     if (cudaGetDevice(&dev) == cudaSuccess)
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const int64_t cap = static_cast<int64_t>(sms) * 8;
-    const int grid = static_cast<int>(T < cap ? T : cap);
-    const int64_t rows_cap = T * k;
-    launch_k(dtype == MOE_BF16 ? combine_grad_kernel<true> : combine_grad_kernel<false>, grid,
-             kThreads, 0, stream, static_cast<const uint8_t *>(dy),
-             static_cast<const uint8_t *>(y_perm), inv_row, topk_w,
-             static_cast<uint8_t *>(dy_perm), dtopk_w, T, d, k, rows_cap, status);
-    count_launches(1);
+    const Args args{static_cast<const uint8_t *>(dy), static_cast<const uint8_t *>(y_perm), inv_row,
+                    topk_w, static_cast<uint8_t *>(dy_perm), dtopk_w, T, d, k, sms, status, stream};
+    if (dtype == MOE_BF16)
+        run_k<true>(args);
+    else
+        run_k<false>(args);
     return cudaGetLastError();
 }
 

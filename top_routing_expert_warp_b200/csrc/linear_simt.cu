@@ -76,44 +76,154 @@ __global__ void __launch_bounds__(kThreads)
                 lin::finish<ACT, TO, T>(ep, i0 + ti + x, static_cast<int>(j0) + tj + y, acc[x][y]);
 }
 
+// V consecutive values as fp32; vec: they lie on a 16-byte boundary (or V = 1).
+template <int V>
+__device__ __forceinline__ void load_v(const float *p, float (&v)[V])
+{
+    if (V % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+            const float4 w = reinterpret_cast<const float4 *>(p)[i];
+            v[4 * i] = w.x;
+            v[(4 * i + 1) % V] = w.y;
+            v[(4 * i + 2) % V] = w.z;
+            v[(4 * i + 3) % V] = w.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            v[i] = p[i];
+    }
+}
+
+template <int V>
+__device__ __forceinline__ void load_v(const __nv_bfloat16 *p, float (&v)[V])
+{
+    if (V == 8) {
+        const uint4 q = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[(2 * i) % V] = __uint_as_float(w[i] << 16);
+            v[(2 * i + 1) % V] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            v[i] = __bfloat162float(p[i]);
+    }
+}
+
+template <int V>
+__device__ __forceinline__ void store_v(float *p, const float (&v)[V])
+{
+    if (V % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i)
+            reinterpret_cast<float4 *>(p)[i] =
+                make_float4(v[4 * i], v[(4 * i + 1) % V], v[(4 * i + 2) % V], v[(4 * i + 3) % V]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            p[i] = v[i];
+    }
+}
+
+template <int V>
+__device__ __forceinline__ void store_v(__nv_bfloat16 *p, const float (&v)[V])
+{
+    if (V == 8) {
+        *reinterpret_cast<uint4 *>(p) =
+            make_uint4(pack_bf16x2(v[0], v[1 % V]), pack_bf16x2(v[2 % V], v[3 % V]),
+                       pack_bf16x2(v[4 % V], v[5 % V]), pack_bf16x2(v[6 % V], v[7 % V]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            p[i] = __float2bfloat16_rn(v[i]);
+    }
+}
+
 // dz = dy * act'(z) in the operand type, and this row block's column sums of
-// the unrounded dz.  One thread per column, rows in order.
-template <typename T, typename TO, int ACT>
+// the unrounded dz, in 32 bits: a warp sums every eighth row of the block's in
+// order, then the eight sums are added in order.  A lane holds V columns (16
+// bytes of the operand type where rows allow it).  Bound by the bytes of dy, z
+// and dz, and for GELU as much by its error function.
+template <typename T, typename TO, int ACT, int V>
 __global__ void __launch_bounds__(kThreads)
     linear_dz_kernel(const TO *__restrict__ dy, int64_t ldy, const T *__restrict__ z, int64_t M,
                      int n, T *__restrict__ dz, int64_t ldz, float *__restrict__ part,
                      int64_t rows_per_block)
 {
     grid_dep_wait();
-    const int col = blockIdx.x * kThreads + threadIdx.x;
-    if (col >= n)
-        return;
+    __shared__ float s_sum[kThreads / 32][32 * V];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int col = (blockIdx.x * 32 + lane) * V;
     const int64_t r0 = blockIdx.y * rows_per_block;
     const int64_t r1 = r0 + rows_per_block < M ? r0 + rows_per_block : M;
-    float sum = 0.0f;
-    for (int64_t r = r0; r < r1; ++r) {
-        float g = lin::to_f32(dy[r * ldy + col]);
-        if (ACT != MOE_LINEAR_NONE)
-            g *= lin::act_bwd<ACT>(lin::to_f32(z[r * n + col]));
-        sum += g;
-        if (dz)
-            lin::put(dz + r * ldz + col, g);
+    float sum[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        sum[i] = 0.0f;
+    if (col < n) {
+#pragma unroll 4
+        for (int64_t r = r0 + warp; r < r1; r += kThreads / 32) {
+            float g[V];
+            load_v<V>(dy + r * ldy + col, g);
+            if (ACT != MOE_LINEAR_NONE) {
+                float zz[V];
+                load_v<V>(z + r * n + col, zz);
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    g[i] *= lin::act_bwd<ACT>(zz[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                sum[i] += g[i];
+            if (dz)
+                store_v<V>(dz + r * ldz + col, g);
+        }
     }
-    if (part)
-        part[static_cast<int64_t>(blockIdx.y) * n + col] = sum;
+    if (part) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            s_sum[warp][lane * V + i] = sum[i];
+        __syncthreads();
+        for (int c = threadIdx.x; c < 32 * V; c += kThreads) {
+            const int at = blockIdx.x * 32 * V + c;
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kThreads / 32; ++w)
+                v += s_sum[w][c];
+            if (at < n)
+                part[static_cast<int64_t>(blockIdx.y) * n + at] = v;
+        }
+    }
 }
 
+// db = the row blocks' sums, added in a fixed order: 32 columns per block,
+// every eighth row block per warp.
 __global__ void __launch_bounds__(kThreads)
     linear_db_kernel(const float *__restrict__ part, int blocks, int n, float *__restrict__ db)
 {
     grid_dep_wait();
-    const int col = blockIdx.x * kThreads + threadIdx.x;
-    if (col >= n)
-        return;
+    __shared__ float s_sum[kThreads / 32][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int col = blockIdx.x * 32 + lane;
     float sum = 0.0f;
-    for (int b = 0; b < blocks; ++b)
-        sum += part[static_cast<int64_t>(b) * n + col];
-    db[col] = sum;
+    if (col < n) {
+#pragma unroll 8
+        for (int b = warp; b < blocks; b += kThreads / 32)
+            sum += part[static_cast<int64_t>(b) * n + col];
+    }
+    s_sum[warp][lane] = sum;
+    __syncthreads();
+    if (warp == 0 && col < n) {
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w)
+            v += s_sum[w][lane];
+        db[col] = v;
+    }
 }
 
 template <typename T, typename TO>
@@ -149,13 +259,23 @@ void run_simt(const LinearGemm &L, cudaStream_t stream)
 template <typename T, typename TO>
 void run_dz(const LinearDz &L, cudaStream_t stream)
 {
+    constexpr int VV = 16 / sizeof(T);
     const int64_t per = (L.M + L.row_blocks - 1) / L.row_blocks;
-    const dim3 grid(static_cast<unsigned>((L.n + kThreads - 1) / kThreads),
+    auto on16 = [](const void *p, int64_t row_bytes) {
+        return reinterpret_cast<uintptr_t>(p) % 16 == 0 && row_bytes % 16 == 0;
+    };
+    const bool vec = L.n % VV == 0 && on16(L.dy, L.ldy * static_cast<int64_t>(sizeof(TO))) &&
+                     on16(L.z, L.n * static_cast<int64_t>(sizeof(T))) &&
+                     on16(L.dz, L.ldz * static_cast<int64_t>(sizeof(T)));
+    const int wide = 32 * (vec ? VV : 1);
+    const dim3 grid(static_cast<unsigned>((L.n + wide - 1) / wide),
                     static_cast<unsigned>(L.row_blocks), 1);
     lin::with_act(L.act, [&](auto a) {
-        launch_k(linear_dz_kernel<T, TO, decltype(a)::value>, grid, kThreads, 0, stream,
-                 static_cast<const TO *>(L.dy), L.ldy, static_cast<const T *>(L.z), L.M, L.n,
-                 static_cast<T *>(L.dz), L.ldz, L.db ? L.part : nullptr, per);
+        auto kernel = vec ? linear_dz_kernel<T, TO, decltype(a)::value, VV>
+                          : linear_dz_kernel<T, TO, decltype(a)::value, 1>;
+        launch_k(kernel, grid, kThreads, 0, stream, static_cast<const TO *>(L.dy), L.ldy,
+                 static_cast<const T *>(L.z), L.M, L.n, static_cast<T *>(L.dz), L.ldz,
+                 L.db ? L.part : nullptr, per);
     });
     count_launches(1);
 }
@@ -184,7 +304,7 @@ cudaError_t launch_linear_dz(const LinearDz &L, cudaStream_t stream)
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !L.db)
         return e;
-    launch_k(linear_db_kernel, dim3((L.n + kThreads - 1) / kThreads), kThreads, 0, stream,
+    launch_k(linear_db_kernel, dim3((L.n + 31) / 32), kThreads, 0, stream,
              static_cast<const float *>(L.part), L.row_blocks, L.n, L.db);
     count_launches(1);
     return cudaGetLastError();

@@ -469,9 +469,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t v[32];
                     tmem_ld32(tacc + c, v);
                     tmem_wait_ld();
+                    const int n = p.J - (j0 + c);        // columns that exist
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        __stcg(mine + (c + i) * 128 + r_local, __uint_as_float(v[i]));
+                        if (i < n)
+                            __stcg(mine + (c + i) * 128 + r_local, __uint_as_float(v[i]));
                 }
                 const int tile = u / p.splits;
                 __threadfence();
@@ -493,11 +495,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             o[i] = 0.0f;
+                        const int n = p.J - (j0 + c);
+#pragma unroll 2
                         for (int s = 0; s < p.splits; ++s) {
                             const float *src = first + static_cast<int64_t>(s) * CG * (ACC * 128);
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                o[i] += __ldcg(src + (c + i) * 128 + r_local);
+                                if (i < n)
+                                    o[i] += __ldcg(src + (c + i) * 128 + r_local);
                         }
                         finish32(p, row, j0 + c, o);
                     }

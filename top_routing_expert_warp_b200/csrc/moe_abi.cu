@@ -1014,14 +1014,21 @@ moe_status moe_linear_backward(const moe_linear_config *cfg, const void *dy, con
     Z.dz = (dx || dW) ? ws + L.dz : nullptr;
     Z.ldz = L.ldz;
     Z.part = reinterpret_cast<float *>(ws + L.db_part);
-    Z.row_blocks = static_cast<int32_t>(c.M < moe::kDzMaxRowBlocks ? c.M : moe::kDzMaxRowBlocks);
+    // row blocks of at least 64 rows (8 for each of a block's warps)
+    Z.row_blocks = static_cast<int32_t>(
+        std::min<int64_t>(moe::kDzMaxRowBlocks, (c.M + 63) / 64));
     Z.db = db;
-    MOE_CUDA(moe::launch_linear_dz(Z, s));
+    // without an activation dz is dy itself, where its type and rows suit the products
+    const bool as_is = !act && c.out_dtype == c.dtype && aligned(dy, 16) && c.ldy * es % 16 == 0;
+    if (as_is)
+        Z.dz = nullptr;
+    if (Z.dz || db)
+        MOE_CUDA(moe::launch_linear_dz(Z, s));
     moe::LinearGemm G{};
     G.dtype = c.dtype;
     G.act = MOE_LINEAR_NONE;
-    G.P = Z.dz;
-    G.ldp = L.ldz;
+    G.P = as_is ? dy : Z.dz;
+    G.ldp = as_is ? c.ldy : L.ldz;
     G.q_kmajor = false;
     G.J = c.n_in;
     linear_scratch(&G, ws, L);
