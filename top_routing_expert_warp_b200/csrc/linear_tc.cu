@@ -470,10 +470,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld32(tacc + c, v);
                     tmem_wait_ld();
                     const int n = p.J - (j0 + c);        // columns that exist
+                    if (n >= 32) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (i < n)
+                        for (int i = 0; i < 32; ++i)
                             __stcg(mine + (c + i) * 128 + r_local, __uint_as_float(v[i]));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (i < n)
+                                __stcg(mine + (c + i) * 128 + r_local, __uint_as_float(v[i]));
+                    }
                 }
                 const int tile = u / p.splits;
                 __threadfence();
@@ -496,13 +502,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int i = 0; i < 32; ++i)
                             o[i] = 0.0f;
                         const int n = p.J - (j0 + c);
-#pragma unroll 2
-                        for (int s = 0; s < p.splits; ++s) {
-                            const float *src = first + static_cast<int64_t>(s) * CG * (ACC * 128);
+                        const float *src = first + c * 128 + r_local;
+                        if (n >= 32) {
+                            for (int s = 0; s < p.splits; ++s, src += CG * (ACC * 128)) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    o[i] += __ldcg(src + i * 128);
+                            }
+                        } else {
+                            // few columns: the loads of the slices in flight together
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                if (i < n)
-                                    o[i] += __ldcg(src + (c + i) * 128 + r_local);
+                                if (i < n) {
+#pragma unroll 8
+                                    for (int s = 0; s < p.splits; ++s)
+                                        o[i] += __ldcg(src + i * 128 + s * (CG * (ACC * 128)));
+                                }
                         }
                         finish32(p, row, j0 + c, o);
                     }
