@@ -295,11 +295,21 @@ struct LinearPlan {
     int splits;              // slices of k per tile
     int64_t tiles;
 };
-constexpr int kLinearMaxTickets = 256;
+constexpr int kLinearMaxTickets = 512;
 LinearPlan linear_plan(int64_t I, int64_t J, int64_t K, bool may_swap);
 size_t linear_plan_part_bytes(const LinearPlan &pl);
 cudaError_t launch_linear_tc(const LinearGemm &L, cudaStream_t stream);
+// fp32 operands on the CUDA cores, and a few rows of either type: see linear_simt.cu.
+struct SimtPlan {
+    int splits;              // slices of k per tile
+    int64_t tiles;
+};
+SimtPlan simt_plan(int64_t I, int64_t J, int64_t K);
+size_t simt_plan_part_bytes(const SimtPlan &pl);
 cudaError_t launch_linear_simt(const LinearGemm &L, cudaStream_t stream);
+// Forward products of at most kLinearRowsMax rows; both operands with k contiguous.
+constexpr int kLinearRowsMax = 4;
+cudaError_t launch_linear_rows(const LinearGemm &L, cudaStream_t stream);
 // dz = dy * act'(z) and its column sums.
 constexpr int kDzMaxRowBlocks = 64;
 struct LinearDz {

@@ -1,5 +1,6 @@
-// Dense products on the CUDA cores, for fp32 operands (TF32 would not meet an
-// fp32 bound), with the projection's epilogue, and the element-wise half of
+// Dense products on the CUDA cores: for fp32 operands (TF32 would not meet an
+// fp32 bound) and, for a few rows of either type, as dot products with the
+// weights' rows; with the projection's epilogue.  And the element-wise half of
 // the projection's gradient.
 //
 //   D[i, j] = sum_k P(i, k) Q(j, k);  out = act(D + bias) + residual
@@ -22,58 +23,303 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int TM = 64, TN = 64, TK = 16;
+constexpr int kGemmThreads = 128;
+constexpr int kPad = 4;                  // floats behind a row of a staged tile
 
-// One 64 x 64 tile per block, 4 x 4 outputs per thread.
-template <typename T, typename TO, int ACT, bool P_K, bool Q_K>
-__global__ void __launch_bounds__(kThreads)
-    linear_simt_kernel(const T *__restrict__ P, int64_t ldp, const T *__restrict__ Q, int64_t ldq,
-                       int64_t I, int J, int64_t K, lin::Epilogue ep)
+// acc (two floats) += a * (b, b).
+__device__ __forceinline__ void fma2(uint64_t &acc, uint64_t a, uint64_t bb)
+{
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(bb));
+}
+
+__device__ __forceinline__ uint64_t twice(float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(b));
+    return r;
+}
+
+// This thread's 8 elements of a 64 x 16 operand tile, as two runs of 4 along
+// the contiguous index: run h starts at (own index, k) = where(h).  Runs that
+// do not lie inside the operand are loaded element by element, zero outside.
+template <bool K_CONTIG>
+struct TileLoad {
+    float v[2][4];
+    __device__ __forceinline__ static void where(int h, int &own, int &k)
+    {
+        const int e = (threadIdx.x + h * kGemmThreads) * 4;
+        own = K_CONTIG ? e / TK : e % 64;
+        k = K_CONTIG ? e % TK : e / 64;
+    }
+    __device__ __forceinline__ void load(const float *__restrict__ src, int64_t ld, int64_t own0,
+                                         int64_t owns, int64_t k0, int64_t k1)
+    {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            int o, kk;
+            where(h, o, kk);
+            const int64_t own = own0 + o, k = k0 + kk;
+            const float *at = K_CONTIG ? src + own * ld + k : src + k * ld + own;
+            const bool inside = own < owns && k < k1;
+            const int64_t left = K_CONTIG ? k1 - k : owns - own;
+            if (inside && left >= 4) {
+                const float4 q = *reinterpret_cast<const float4 *>(at);
+                v[h][0] = q.x;
+                v[h][1] = q.y;
+                v[h][2] = q.z;
+                v[h][3] = q.w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[h][i] = inside && i < left ? at[i] : 0.0f;
+            }
+        }
+    }
+    __device__ __forceinline__ void store(float (*dst)[64 + kPad]) const
+    {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            int o, kk;
+            where(h, o, kk);
+            if (K_CONTIG) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    dst[kk + i][o] = v[h][i];
+            } else {
+                *reinterpret_cast<float4 *>(&dst[kk][o]) =
+                    make_float4(v[h][0], v[h][1], v[h][2], v[h][3]);
+            }
+        }
+    }
+};
+
+struct SimtParams {
+    const float *P, *Q;
+    int64_t ldp, ldq;
+    int64_t I, K;
+    int32_t J, i_tiles, splits, act;
+    lin::Epilogue ep;
+    float *part;             // [units][64][64]
+    uint32_t *tickets;       // [tiles], zero between launches
+};
+
+__device__ __forceinline__ float act_any(int act, float z)
+{
+    switch (act) {
+    case MOE_LINEAR_RELU: return lin::act_fwd<MOE_LINEAR_RELU>(z);
+    case MOE_LINEAR_SILU: return lin::act_fwd<MOE_LINEAR_SILU>(z);
+    case MOE_LINEAR_GELU: return lin::act_fwd<MOE_LINEAR_GELU>(z);
+    case MOE_LINEAR_GELU_TANH: return lin::act_fwd<MOE_LINEAR_GELU_TANH>(z);
+    default: return z;
+    }
+}
+
+// A 64 x 64 tile (or a slice of its k range) per block, 8 x 4 outputs per
+// thread in pairs of rows (fma.rn.f32x2: two products per issue, so that the
+// shared-memory reads have issue slots left), the next 16 of k in registers
+// while the present ones are multiplied.  Bound by the fp32 pipes for large
+// products.  Tiles too few to fill the GPU are cut along k; the slices' sums go
+// through the workspace and the last block to finish adds them in slice order
+// (a ticket per tile, which wraps to 0).
+template <bool P_K, bool Q_K>
+__global__ void __launch_bounds__(kGemmThreads) linear_simt_kernel(const __grid_constant__ SimtParams p)
 {
     grid_dep_wait();
-    __shared__ float s_p[TK][TM + 4], s_q[TK][TN + 4];
+    __shared__ __align__(16) float s_p[2][TK][TM + kPad];
+    __shared__ __align__(16) float s_q[2][TK][TN + kPad];
+    __shared__ uint32_t s_last;
     const int tid = threadIdx.x;
-    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * TM;
-    const int64_t j0 = static_cast<int64_t>(blockIdx.y) * TN;
-    const int ti = (tid >> 4) * 4, tj = (tid & 15) * 4;
-    float acc[4][4] = {};
-    for (int64_t k0 = 0; k0 < K; k0 += TK) {
-        for (int e = tid; e < TM * TK; e += kThreads) {
-            const int i = P_K ? e / TK : e % TM, k = P_K ? e % TK : e / TM;
-            float v = 0.0f;
-            if (i0 + i < I && k0 + k < K)
-                v = lin::to_f32(P_K ? P[(i0 + i) * ldp + k0 + k] : P[(k0 + k) * ldp + i0 + i]);
-            s_p[k][i] = v;
+    const int64_t unit = blockIdx.x;
+    const int64_t tile = unit / p.splits;
+    const int slice = static_cast<int>(unit - tile * p.splits);
+    const int64_t jt = tile / p.i_tiles;
+    const int64_t i0 = (tile - jt * p.i_tiles) * TM, j0 = jt * TN;
+    const int64_t steps = (p.K + TK - 1) / TK;
+    const int64_t kb = steps * slice / p.splits * TK;
+    const int64_t ke = steps * (slice + 1) / p.splits * TK;
+    const int64_t k1 = ke < p.K ? ke : p.K;
+    const int ti = (tid >> 4) * 8, tj = (tid & 15) * 4;
+    uint64_t acc[4][4] = {};                 // [row pair][column]
+    TileLoad<P_K> lp;
+    TileLoad<Q_K> lq;
+    lp.load(p.P, p.ldp, i0, p.I, kb, k1);
+    lq.load(p.Q, p.ldq, j0, p.J, kb, k1);
+    lp.store(s_p[0]);
+    lq.store(s_q[0]);
+    __syncthreads();
+    int cur = 0;
+    for (int64_t k0 = kb; k0 < k1; k0 += TK, cur ^= 1) {
+        const bool more = k0 + TK < k1;
+        if (more) {
+            lp.load(p.P, p.ldp, i0, p.I, k0 + TK, k1);
+            lq.load(p.Q, p.ldq, j0, p.J, k0 + TK, k1);
         }
-        for (int e = tid; e < TN * TK; e += kThreads) {
-            const int j = Q_K ? e / TK : e % TN, k = Q_K ? e % TK : e / TN;
-            float v = 0.0f;
-            if (j0 + j < J && k0 + k < K)
-                v = lin::to_f32(Q_K ? Q[(j0 + j) * ldq + k0 + k] : Q[(k0 + k) * ldq + j0 + j]);
-            s_q[k][j] = v;
-        }
-        __syncthreads();
 #pragma unroll
         for (int k = 0; k < TK; ++k) {
-            float a[4], b[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                a[x] = s_p[k][ti + x];
-                b[x] = s_q[k][tj + x];
-            }
+            const ulonglong2 a0 = *reinterpret_cast<const ulonglong2 *>(&s_p[cur][k][ti]);
+            const ulonglong2 a1 = *reinterpret_cast<const ulonglong2 *>(&s_p[cur][k][ti + 4]);
+            const float4 b = *reinterpret_cast<const float4 *>(&s_q[cur][k][tj]);
+            const uint64_t a[4] = {a0.x, a0.y, a1.x, a1.y};
+            const uint64_t bb[4] = {twice(b.x), twice(b.y), twice(b.z), twice(b.w)};
 #pragma unroll
             for (int x = 0; x < 4; ++x)
 #pragma unroll
                 for (int y = 0; y < 4; ++y)
-                    acc[x][y] = fmaf(a[x], b[y], acc[x][y]);
+                    fma2(acc[x][y], a[x], bb[y]);
+        }
+        if (more) {
+            lp.store(s_p[cur ^ 1]);
+            lq.store(s_q[cur ^ 1]);
         }
         __syncthreads();
     }
+    float out[8][4];
 #pragma unroll
     for (int x = 0; x < 4; ++x)
 #pragma unroll
-        for (int y = 0; y < 4; ++y)
-            if (i0 + ti + x < I && j0 + tj + y < J)
-                lin::finish<ACT, TO, T>(ep, i0 + ti + x, static_cast<int>(j0) + tj + y, acc[x][y]);
+        for (int y = 0; y < 4; ++y) {
+            out[2 * x][y] = __uint_as_float(static_cast<uint32_t>(acc[x][y]));
+            out[2 * x + 1][y] = __uint_as_float(static_cast<uint32_t>(acc[x][y] >> 32));
+        }
+    if (p.splits > 1) {
+        float4 *mine = reinterpret_cast<float4 *>(p.part) + unit * (TM * TN / 4) + tid;
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+            __stcg(mine + x * kGemmThreads, make_float4(out[x][0], out[x][1], out[x][2], out[x][3]));
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) {
+            s_last = atomicInc(p.tickets + tile, p.splits - 1) == static_cast<uint32_t>(p.splits - 1);
+            __threadfence();
+        }
+        __syncthreads();
+        if (!s_last)
+            return;
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                out[x][y] = 0.0f;
+        const float4 *first = reinterpret_cast<const float4 *>(p.part) +
+                              tile * p.splits * (TM * TN / 4) + tid;
+        for (int s = 0; s < p.splits; ++s) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const float4 v = __ldcg(first + s * (TM * TN / 4) + x * kGemmThreads);
+                out[x][0] += v.x;
+                out[x][1] += v.y;
+                out[x][2] += v.z;
+                out[x][3] += v.w;
+            }
+        }
+    }
+    const lin::Epilogue &ep = p.ep;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+        const int64_t row = i0 + ti + x;
+        if (row >= p.I)
+            continue;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            const int64_t col = j0 + tj + y;
+            if (col >= p.J)
+                continue;
+            float z = out[x][y];
+            if (ep.bias)
+                z += __ldg(ep.bias + col);
+            if (ep.preact)
+                static_cast<float *>(ep.preact)[row * ep.cols + col] = z;
+            z = act_any(p.act, z);
+            if (ep.residual)
+                z += static_cast<const float *>(ep.residual)[row * ep.ldr + col];
+            static_cast<float *>(ep.out)[row * ep.ldo + col] = z;
+        }
+    }
+}
+
+// Few rows (serving): y[m, n] = act(sum_k x[m, k] W[n, k] + bias) + residual.
+// WPR warps per output n read its weights once, 16 bytes per lane with 8 loads
+// in flight, next to the same places of the rows of x (in L1); the warps' sums
+// are added in order.  Bound by the weights' bytes.
+template <typename T, typename TO, int MR>
+__global__ void __launch_bounds__(kThreads)
+    linear_rows_kernel(const T *__restrict__ x, int64_t ldx, const T *__restrict__ W, int M, int K,
+                       int N, int wpr, int act, const __grid_constant__ lin::Epilogue ep)
+{
+    grid_dep_wait();
+    constexpr int V = 16 / sizeof(T);
+    constexpr int U = 8 / MR < 2 ? 2 : 8 / MR;
+    __shared__ float s_sum[kThreads / 32][MR];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int part = warp % wpr;
+    const int n = blockIdx.x * (kThreads / 32 / wpr) + warp / wpr;
+    const int chunks = K / V;
+    float acc[MR];
+#pragma unroll
+    for (int m = 0; m < MR; ++m)
+        acc[m] = 0.0f;
+    if (n < N) {
+        const uint4 *w = reinterpret_cast<const uint4 *>(W + static_cast<int64_t>(n) * K);
+        const int step = 32 * wpr;
+        for (int c0 = part * 32 + lane; c0 < chunks; c0 += step * U) {
+            uint4 wq[U], xq[MR][U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int c = c0 + u * step;
+                wq[u] = c < chunks ? __ldcs(w + c) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int m = 0; m < MR; ++m)
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int c = c0 + u * step;
+                    xq[m][u] = m < M && c < chunks
+                                   ? __ldg(reinterpret_cast<const uint4 *>(x + m * ldx) + c)
+                                   : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const uint32_t a[4] = {wq[u].x, wq[u].y, wq[u].z, wq[u].w};
+#pragma unroll
+                for (int m = 0; m < MR; ++m) {
+                    const uint32_t b[4] = {xq[m][u].x, xq[m][u].y, xq[m][u].z, xq[m][u].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (sizeof(T) == 2) {
+                            acc[m] = fmaf(__uint_as_float(a[i] << 16), __uint_as_float(b[i] << 16),
+                                          acc[m]);
+                            acc[m] = fmaf(__uint_as_float(a[i] & 0xFFFF0000u),
+                                          __uint_as_float(b[i] & 0xFFFF0000u), acc[m]);
+                        } else {
+                            acc[m] = fmaf(__uint_as_float(a[i]), __uint_as_float(b[i]), acc[m]);
+                        }
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < MR; ++m) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            acc[m] += __shfl_xor_sync(0xffffffffu, acc[m], o);
+        if (lane == 0)
+            s_sum[warp][m] = acc[m];
+    }
+    __syncthreads();
+    if (part != 0 || n >= N || lane >= M)
+        return;
+    float z = 0.0f;
+    for (int w = 0; w < wpr; ++w)
+        z += s_sum[warp + w][lane];
+    if (ep.bias)
+        z += ep.bias[n];
+    if (ep.preact)
+        lin::put(static_cast<T *>(ep.preact) + static_cast<int64_t>(lane) * ep.cols + n, z);
+    z = act_any(act, z);
+    if (ep.residual)
+        z += lin::to_f32(static_cast<const TO *>(ep.residual)[lane * ep.ldr + n]);
+    lin::put(static_cast<TO *>(ep.out) + lane * ep.ldo + n, z);
 }
 
 // V consecutive values as fp32; vec: they lie on a 16-byte boundary (or V = 1).
@@ -226,13 +472,8 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
-template <typename T, typename TO>
-void run_simt(const LinearGemm &L, cudaStream_t stream)
+lin::Epilogue epilogue_of(const LinearGemm &L)
 {
-    const dim3 grid(static_cast<unsigned>((L.I + TM - 1) / TM),
-                    static_cast<unsigned>((L.J + TN - 1) / TN), 1);
-    const T *P = static_cast<const T *>(L.P);
-    const T *Q = static_cast<const T *>(L.Q);
     lin::Epilogue ep;
     ep.out = L.out;
     ep.ldo = L.ldo;
@@ -242,17 +483,22 @@ void run_simt(const LinearGemm &L, cudaStream_t stream)
     ep.preact = L.preact;
     ep.rows = static_cast<int32_t>(L.I);
     ep.cols = L.J;
-    if (L.p_kmajor && L.q_kmajor)
-        lin::with_act(L.act, [&](auto a) {
-            launch_k(linear_simt_kernel<T, TO, decltype(a)::value, true, true>, grid, kThreads, 0,
-                     stream, P, L.ldp, Q, L.ldq, L.I, L.J, L.K, ep);
-        });
-    else if (L.p_kmajor)
-        launch_k(linear_simt_kernel<T, TO, MOE_LINEAR_NONE, true, false>, grid, kThreads, 0,
-                 stream, P, L.ldp, Q, L.ldq, L.I, L.J, L.K, ep);
-    else
-        launch_k(linear_simt_kernel<T, TO, MOE_LINEAR_NONE, false, false>, grid, kThreads, 0,
-                 stream, P, L.ldp, Q, L.ldq, L.I, L.J, L.K, ep);
+    return ep;
+}
+
+template <typename T, typename TO>
+void run_rows(const LinearGemm &L, cudaStream_t stream)
+{
+    // warps per output so that about 16 warps run on each SM
+    int wpr = 1;
+    while (wpr < 8 && static_cast<int64_t>(L.J) * wpr < 148 * 16)
+        wpr *= 2;
+    const int per = kThreads / 32 / wpr;
+    auto kernel = L.I == 1 ? linear_rows_kernel<T, TO, 1>
+                           : (L.I == 2 ? linear_rows_kernel<T, TO, 2> : linear_rows_kernel<T, TO, 4>);
+    launch_k(kernel, dim3((L.J + per - 1) / per), kThreads, 0, stream, static_cast<const T *>(L.P),
+             L.ldp, static_cast<const T *>(L.Q), static_cast<int>(L.I), static_cast<int>(L.K), L.J,
+             wpr, L.act, epilogue_of(L));
     count_launches(1);
 }
 
@@ -282,14 +528,59 @@ void run_dz(const LinearDz &L, cudaStream_t stream)
 
 }  // namespace
 
+SimtPlan simt_plan(int64_t I, int64_t J, int64_t K)
+{
+    SimtPlan pl;
+    pl.tiles = (I + TM - 1) / TM * ((J + TN - 1) / TN);
+    // about four blocks per SM, slices of at least 48 of k
+    int64_t s = 148 * 4 / pl.tiles;
+    if (s > K / 48)
+        s = K / 48;
+    pl.splits = static_cast<int>(s < 1 ? 1 : s);
+    return pl;
+}
+
+size_t simt_plan_part_bytes(const SimtPlan &pl)
+{
+    return pl.splits > 1 ? static_cast<size_t>(pl.tiles) * pl.splits * TM * TN * 4 : 0;
+}
+
 cudaError_t launch_linear_simt(const LinearGemm &L, cudaStream_t stream)
 {
+    const SimtPlan pl = simt_plan(L.I, L.J, L.K);
+    const int64_t units = pl.tiles * pl.splits;
+    if (units > 0x7FFFFFFF)
+        return cudaErrorInvalidValue;
+    SimtParams p;
+    p.P = static_cast<const float *>(L.P);
+    p.Q = static_cast<const float *>(L.Q);
+    p.ldp = L.ldp;
+    p.ldq = L.ldq;
+    p.I = L.I;
+    p.K = L.K;
+    p.J = L.J;
+    p.i_tiles = static_cast<int32_t>((L.I + TM - 1) / TM);
+    p.splits = pl.splits;
+    p.act = L.act;
+    p.ep = epilogue_of(L);
+    p.part = L.part;
+    p.tickets = L.tickets;
+    auto kernel = L.p_kmajor ? (L.q_kmajor ? linear_simt_kernel<true, true>
+                                           : linear_simt_kernel<true, false>)
+                             : linear_simt_kernel<false, false>;
+    launch_k(kernel, dim3(static_cast<unsigned>(units)), kGemmThreads, 0, stream, p);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_linear_rows(const LinearGemm &L, cudaStream_t stream)
+{
     if (L.dtype == MOE_F32)
-        run_simt<float, float>(L, stream);
+        run_rows<float, float>(L, stream);
     else if (L.out_f32)
-        run_simt<__nv_bfloat16, float>(L, stream);
+        run_rows<__nv_bfloat16, float>(L, stream);
     else
-        run_simt<__nv_bfloat16, __nv_bfloat16>(L, stream);
+        run_rows<__nv_bfloat16, __nv_bfloat16>(L, stream);
     return cudaGetLastError();
 }
 

@@ -486,10 +486,12 @@ LinearLayout linear_layout(const moe_linear_config &c, bool backward)
     const int64_t es = elem_size(c.dtype);
     L.ldz = (c.n_out + 7) / 8 * 8;
     L.status = take(256);
-    if (c.dtype == MOE_BF16 && c.M > 0) {
+    if (c.M > 0) {
         L.tickets = take(moe::kLinearMaxTickets * sizeof(uint32_t));
-        auto part = [](int64_t I, int64_t J, int64_t K, bool swap) {
-            return moe::linear_plan_part_bytes(moe::linear_plan(I, J, K, swap));
+        auto part = [&](int64_t I, int64_t J, int64_t K, bool swap) {
+            return c.dtype == MOE_BF16
+                       ? moe::linear_plan_part_bytes(moe::linear_plan(I, J, K, swap))
+                       : moe::simt_plan_part_bytes(moe::simt_plan(I, J, K));
         };
         size_t most = part(c.M, c.n_out, c.n_in, true);
         if (backward) {
@@ -515,6 +517,8 @@ void linear_scratch(moe::LinearGemm *G, uint8_t *ws, const LinearLayout &L)
 
 cudaError_t launch_linear(const moe::LinearGemm &G, cudaStream_t s)
 {
+    if (G.I <= moe::kLinearRowsMax && G.p_kmajor && G.q_kmajor)
+        return moe::launch_linear_rows(G, s);
     return G.dtype == MOE_BF16 ? moe::launch_linear_tc(G, s) : moe::launch_linear_simt(G, s);
 }
 
