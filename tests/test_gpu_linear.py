@@ -15,7 +15,8 @@ ACTS = ["none", "relu", "silu", "gelu", "gelu_tanh"]
 SHAPES = [(1, 8, 1, 0), (1, 1024, 264, 0), (2, 520, 130, 8), (7, 64, 33, 0), (16, 2048, 512, 0),
           (17, 72, 129, 16), (63, 136, 255, 0), (64, 4096, 64, 8), (100, 264, 96, 0),
           (129, 1032, 257, 8), (256, 256, 256, 0), (300, 520, 1000, 0), (513, 192, 520, 24),
-          (1030, 328, 72, 0), (1000, 2056, 1500, 0), (2100, 520, 2561, 8), (40, 4096, 4096, 0)]
+          (1030, 328, 72, 0), (1000, 2056, 1500, 0), (2100, 520, 2561, 8), (40, 4096, 4096, 0), (640, 512, 384, 0),
+          (384, 1024, 384, 0), (400, 648, 776, 8)]
 
 
 def strided(t, pad, fill=7.0):
@@ -214,7 +215,8 @@ def test_linear_keeps_nan_and_inf_to_their_rows(dt, M):
     assert torch.equal(y.cpu()[~bad].double(), want[~bad])
 
 
-@pytest.mark.parametrize("shape", [(1, 2048, 1000), (24, 4096, 300), (200, 4096, 129), (640, 512, 384)], ids=str)
+@pytest.mark.parametrize("shape", [(1, 2048, 1000), (24, 4096, 300), (200, 4096, 129), (640, 512, 384),
+                                   (384, 1024, 384), (512, 640, 640)], ids=str)
 def test_linear_is_the_same_twice(shape):
     M, K, N = shape
     g = torch.Generator().manual_seed(1)

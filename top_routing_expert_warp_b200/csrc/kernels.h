@@ -282,28 +282,18 @@ struct LinearGemm {
     const void *residual;
     int64_t ldr;
     void *preact;            // [I, J]
-    float *part;             // partial tiles, linear_plan_part_bytes (bf16 operands)
-    uint32_t *tickets;       // kLinearMaxTickets words, zero between launches
+    float *part;             // partial tiles, simt_plan_part_bytes (fp32 operands)
+    uint32_t *tickets;       // kLinearMaxTickets words, zero between launches (fp32 operands)
     uint32_t *status;
 };
-// bf16 operands on the tensor cores: see linear_tc.cu.  The plan, and with it
-// the workspace, depends on the sizes alone.
-struct LinearPlan {
-    int cg;                  // CTAs per tile
-    bool swap;               // the transposed product
-    int bn;                  // tile columns
-    int splits;              // slices of k per tile
-    int64_t tiles;
-};
-constexpr int kLinearMaxTickets = 512;
-LinearPlan linear_plan(int64_t I, int64_t J, int64_t K, bool may_swap);
-size_t linear_plan_part_bytes(const LinearPlan &pl);
+// bf16 operands on the tensor cores: see linear_tc.cu.
 cudaError_t launch_linear_tc(const LinearGemm &L, cudaStream_t stream);
 // fp32 operands on the CUDA cores, and a few rows of either type: see linear_simt.cu.
 struct SimtPlan {
     int splits;              // slices of k per tile
     int64_t tiles;
 };
+constexpr int kLinearMaxTickets = 512;
 SimtPlan simt_plan(int64_t I, int64_t J, int64_t K);
 size_t simt_plan_part_bytes(const SimtPlan &pl);
 cudaError_t launch_linear_simt(const LinearGemm &L, cudaStream_t stream);

@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kThreads)
 {
     grid_dep_wait();
     constexpr int V = 16 / sizeof(T);
-    constexpr int U = 8 / MR < 2 ? 2 : 8 / MR;
+    constexpr int U = 8;
     __shared__ float s_sum[kThreads / 32][MR];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int part = warp % wpr;
@@ -262,27 +262,24 @@ __global__ void __launch_bounds__(kThreads)
         const uint4 *w = reinterpret_cast<const uint4 *>(W + static_cast<int64_t>(n) * K);
         const int step = 32 * wpr;
         for (int c0 = part * 32 + lane; c0 < chunks; c0 += step * U) {
-            uint4 wq[U], xq[MR][U];
+            uint4 wq[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int c = c0 + u * step;
                 wq[u] = c < chunks ? __ldcs(w + c) : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
-            for (int m = 0; m < MR; ++m)
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int c = c0 + u * step;
-                    xq[m][u] = m < M && c < chunks
-                                   ? __ldg(reinterpret_cast<const uint4 *>(x + m * ldx) + c)
-                                   : make_uint4(0, 0, 0, 0);
-                }
-#pragma unroll
             for (int u = 0; u < U; ++u) {
                 const uint32_t a[4] = {wq[u].x, wq[u].y, wq[u].z, wq[u].w};
+                const int c = c0 + u * step;
+                if (c >= chunks)
+                    break;
 #pragma unroll
                 for (int m = 0; m < MR; ++m) {
-                    const uint32_t b[4] = {xq[m][u].x, xq[m][u].y, xq[m][u].z, xq[m][u].w};
+                    if (m >= M)
+                        break;
+                    const uint4 xq = __ldg(reinterpret_cast<const uint4 *>(x + m * ldx) + c);
+                    const uint32_t b[4] = {xq.x, xq.y, xq.z, xq.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         if (sizeof(T) == 2) {
@@ -489,9 +486,9 @@ lin::Epilogue epilogue_of(const LinearGemm &L)
 template <typename T, typename TO>
 void run_rows(const LinearGemm &L, cudaStream_t stream)
 {
-    // warps per output so that about 16 warps run on each SM
+    // warps per output so that at least 24 warps run on each SM
     int wpr = 1;
-    while (wpr < 8 && static_cast<int64_t>(L.J) * wpr < 148 * 16)
+    while (wpr < 8 && static_cast<int64_t>(L.J) * wpr < 148 * 24)
         wpr *= 2;
     const int per = kThreads / 32 / wpr;
     auto kernel = L.I == 1 ? linear_rows_kernel<T, TO, 1>

@@ -8,7 +8,7 @@
 // with k contiguous is staged as rows of 64 k (128-byte swizzle), one with its
 // own index contiguous as blocks of 64 of that index by 64 k.
 //
-// A unit of work is a tile, or one of `splits` slices of a tile's k range:
+// A tile is
 //   CG = 2: 256 x 256 on a CTA pair (cta_group::2, each CTA stages 128 rows of
 //           P and 128 of Q), for large products: per SM a 64-wide k block
 //           brings 32 KB for 256 cycles of tensor work;
@@ -17,14 +17,24 @@
 // (128 of them are the MMA's rows) and Q the tokens (rounded up to 16 as the
 // MMA's columns), so the weights are read once at the rate of HBM and no MMA
 // is spent on absent tokens.
-// Slices of one tile leave fp32 partial tiles in the workspace; the last one to
-// finish (a ticket per tile, which wraps to 0 by itself) adds them in slice
-// order, so the result does not depend on which was last.
+// Tiles too few for the GPU are cut along k into slices, each on its own CTA
+// (or pair) of one cluster of at most 8.  The slices' sums meet in shared memory:
+// every CTA of the cluster takes a share of the columns, the others send it
+// theirs (distributed shared memory, in the space of the finished stages), and
+// it adds them in slice order and finishes them.  Through global memory with
+// a ticket this took 4-12 us per launch instead of 2.
 //
 // Roles: warp 0 TMA producer, warp 1 MMA issuer, warps 2-9 epilogue (two per
 // TMEM lane quarter, on alternate 32-column steps).  Two accumulators in TMEM:
-// the epilogue of a tile overlaps the products of the next.  Every wait is
-// bounded.
+// without slices the epilogue of a tile overlaps the products of the next; a
+// slice uses both for the halves of its k range, since the tensor cores' fp32
+// sums are cut (not rounded) at every step and their error grows with the
+// length of the chain.  Every wait is bounded.
+//
+// A lane of the epilogue holds a piece of a row and writes it 16 bytes at a
+// time.  Where rows are not 16-byte aligned the warp first turns its 32 x 32
+// accumulators over in shared memory, so that its lanes hold consecutive
+// columns (element-wise stores of row pieces cost 15 us more at 300 x 300).
 #include "common.cuh"
 #include "kernels.h"
 #include "linear.cuh"
@@ -41,22 +51,25 @@ constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int STAGES = 6;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kTurn = 33;                // floats between the columns of a turned-over block
+constexpr int TURN_BYTES = kEpiWarps * 32 * kTurn * 4;
 constexpr int AUX_BYTES = 8 * (2 * STAGES + 5) + 32;
-constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + AUX_BYTES;
+constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + TURN_BYTES + AUX_BYTES;
+static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of a block");
 
 struct TcParams {
     int32_t I, J;            // rows and columns of D
-    int32_t i_tiles, j_tiles;
-    int32_t units, splits;
+    int32_t i_tiles, tiles;
+    int32_t slices;
+    int32_t share;           // columns of a tile that a slice's CTA finishes, even
     int32_t kblocks;
     int32_t bn;              // columns of the MMA (CG = 1), multiple of 16
     int32_t b_bytes;         // bytes of Q per CTA and stage
     int32_t act;
     int32_t swap;            // D is the output's transpose
-    int32_t out_f32, out_vec, res_vec, pre_vec;
+    int32_t out_f32;
+    int32_t vec;             // rows of every output start on 16-byte boundaries
     lin::Epilogue ep;        // in terms of the output
-    float *part;             // [units][CG][128 CG columns][128 rows]
-    uint32_t *tickets;       // [tiles][CG], zero between launches
     uint32_t *status;
 };
 
@@ -78,159 +91,178 @@ __device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t saddr)
 // Bits 15 and 16 of the instruction descriptor: A, B with their own index contiguous.
 constexpr uint32_t kIdescTransA = 1u << 15, kIdescTransB = 1u << 16;
 
+template <int ACT>
+__device__ __forceinline__ void act_all(float (&v)[32])
+{
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        v[i] = lin::act_fwd<ACT>(v[i]);
+}
+
 __device__ __forceinline__ void act32(int act, float (&v)[32])
 {
-#define MOE_ACT32(A)                          \
-    _Pragma("unroll") for (int i = 0; i < 32; ++i) v[i] = lin::act_fwd<A>(v[i]);
     switch (act) {
-    case MOE_LINEAR_RELU: MOE_ACT32(MOE_LINEAR_RELU) break;
-    case MOE_LINEAR_SILU: MOE_ACT32(MOE_LINEAR_SILU) break;
-    case MOE_LINEAR_GELU: MOE_ACT32(MOE_LINEAR_GELU) break;
-    case MOE_LINEAR_GELU_TANH: MOE_ACT32(MOE_LINEAR_GELU_TANH) break;
+    case MOE_LINEAR_RELU: act_all<MOE_LINEAR_RELU>(v); break;
+    case MOE_LINEAR_SILU: act_all<MOE_LINEAR_SILU>(v); break;
+    case MOE_LINEAR_GELU: act_all<MOE_LINEAR_GELU>(v); break;
+    case MOE_LINEAR_GELU_TANH: act_all<MOE_LINEAR_GELU_TANH>(v); break;
     default: break;
     }
-#undef MOE_ACT32
 }
 
-// 32 consecutive values of a row to bf16 or fp32.
-__device__ __forceinline__ void store32(void *base, int64_t at, bool f32, bool vec, int n,
-                                        const float (&v)[32])
+// n (a multiple of 8, at most 32) consecutive values of a row that starts on a
+// 16-byte boundary.
+__device__ __forceinline__ void store_run(void *base, int64_t at, bool f32, int n,
+                                          const float (&v)[32])
 {
-    if (f32) {
-        float *p = static_cast<float *>(base) + at;
-        if (vec && n == 32) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    for (int i = 0; i < 32; i += 8) {
+        if (i >= n)
+            continue;
+        if (f32) {
+            float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(base) + at + i);
+            p[0] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            p[1] = make_float4(v[i + 4], v[i + 5], v[i + 6], v[i + 7]);
         } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (i < n)
-                    p[i] = v[i];
-        }
-    } else {
-        __nv_bfloat16 *p = static_cast<__nv_bfloat16 *>(base) + at;
-        if (vec && n == 32) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-                uint4 w;
-                w.x = pack_bf16x2(v[i], v[i + 1]);
-                w.y = pack_bf16x2(v[i + 2], v[i + 3]);
-                w.z = pack_bf16x2(v[i + 4], v[i + 5]);
-                w.w = pack_bf16x2(v[i + 6], v[i + 7]);
-                *reinterpret_cast<uint4 *>(p + i) = w;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (i < n)
-                    p[i] = __float2bfloat16_rn(v[i]);
+            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(base) + at + i) =
+                make_uint4(pack_bf16x2(v[i], v[i + 1]), pack_bf16x2(v[i + 2], v[i + 3]),
+                           pack_bf16x2(v[i + 4], v[i + 5]), pack_bf16x2(v[i + 6], v[i + 7]));
         }
     }
 }
 
-// v += 32 consecutive values of a row.
-__device__ __forceinline__ void add32(const void *base, int64_t at, bool f32, bool vec, int n,
-                                      float (&v)[32])
+__device__ __forceinline__ void add_run(const void *base, int64_t at, bool f32, int n, float (&v)[32])
 {
-    if (f32) {
-        const float *p = static_cast<const float *>(base) + at;
-        if (vec && n == 32) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-                const float4 w = *reinterpret_cast<const float4 *>(p + i);
-                v[i] += w.x;
-                v[i + 1] += w.y;
-                v[i + 2] += w.z;
-                v[i + 3] += w.w;
+    for (int i = 0; i < 32; i += 8) {
+        if (i >= n)
+            continue;
+        if (f32) {
+            const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + at + i);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float4 w = p[h];
+                v[i + 4 * h] += w.x;
+                v[i + 4 * h + 1] += w.y;
+                v[i + 4 * h + 2] += w.z;
+                v[i + 4 * h + 3] += w.w;
             }
         } else {
+            const uint4 q =
+                *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(base) + at + i);
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (i < n)
-                    v[i] += p[i];
-        }
-    } else {
-        const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(base) + at;
-        if (vec && n == 32) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-                const uint4 q = *reinterpret_cast<const uint4 *>(p + i);
-                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    v[i + 2 * x] += __uint_as_float(w[x] << 16);
-                    v[i + 2 * x + 1] += __uint_as_float(w[x] & 0xFFFF0000u);
-                }
+            for (int x = 0; x < 4; ++x) {
+                v[i + 2 * x] += __uint_as_float(w[x] << 16);
+                v[i + 2 * x + 1] += __uint_as_float(w[x] & 0xFFFF0000u);
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (i < n)
-                    v[i] += __bfloat162float(p[i]);
         }
     }
 }
 
-// One thread's 32 accumulators (row r of D, columns c0..) to the output.
-__device__ __forceinline__ void finish32(const TcParams &p, int64_t r, int c0, float (&v)[32])
+__device__ __forceinline__ float load1(const void *base, int64_t at, bool f32)
+{
+    return f32 ? static_cast<const float *>(base)[at]
+               : __bfloat162float(static_cast<const __nv_bfloat16 *>(base)[at]);
+}
+
+__device__ __forceinline__ void store1(void *base, int64_t at, bool f32, float v)
+{
+    if (f32)
+        static_cast<float *>(base)[at] = v;
+    else
+        static_cast<__nv_bfloat16 *>(base)[at] = __float2bfloat16_rn(v);
+}
+
+// 32 values of this lane, as elements at + i * step, n of them: bias added.
+__device__ __forceinline__ void finish_run(const TcParams &p, int64_t out, int64_t out_step,
+                                           int64_t res, int64_t res_step, int64_t pre,
+                                           int64_t pre_step, int n, float (&v)[32])
 {
     const lin::Epilogue &ep = p.ep;
-    if (r >= p.I || c0 >= p.J)
-        return;
-    const int n = p.J - c0 < 32 ? p.J - c0 : 32;
-    if (!p.swap) {
-        if (ep.bias) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (i < n)
-                    v[i] += __ldg(ep.bias + c0 + i);
-        }
-        if (ep.preact)
-            store32(ep.preact, r * ep.cols + c0, false, p.pre_vec, n, v);
-        act32(p.act, v);
-        if (ep.residual)
-            add32(ep.residual, r * ep.ldr + c0, p.out_f32, p.res_vec, n, v);
-        store32(ep.out, r * ep.ldo + c0, p.out_f32, p.out_vec, n, v);
-    } else {
-        // r is the output's column (consecutive over the lanes), c0 + i its row
-        const float b = ep.bias ? __ldg(ep.bias + r) : 0.0f;
+    if (ep.preact) {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-            v[i] += b;
-        if (ep.preact) {
+            if (i < n)
+                store1(ep.preact, pre + i * pre_step, false, v[i]);
+    }
+    act32(p.act, v);
+    if (ep.residual) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < n)
+                v[i] += load1(ep.residual, res + i * res_step, p.out_f32);
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        if (i < n)
+            store1(ep.out, out + i * out_step, p.out_f32, v[i]);
+}
+
+// One warp's 32 rows of D from row0 on (one per lane), nc (at most 32) columns
+// from c0 on; st: 32 x kTurn floats of this warp.
+__device__ __forceinline__ void finish_block(const TcParams &p, float *st, int64_t row0, int c0,
+                                             int nc, float (&v)[32])
+{
+    const int lane = threadIdx.x & 31;
+    const lin::Epilogue &ep = p.ep;
+    const int n = p.J - c0 < nc ? p.J - c0 : nc;
+    const int64_t r = row0 + lane;
+    if (p.swap) {
+        // the lanes are consecutive columns of the output, the columns its rows
+        if (r < p.I) {
+            const float b = ep.bias ? __ldg(ep.bias + r) : 0.0f;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-                if (i < n)
-                    static_cast<__nv_bfloat16 *>(ep.preact)[static_cast<int64_t>(c0 + i) * ep.cols + r] =
-                        __float2bfloat16_rn(v[i]);
+                v[i] += b;
+            finish_run(p, c0 * ep.ldo + r, ep.ldo, c0 * ep.ldr + r, ep.ldr,
+                       static_cast<int64_t>(c0) * ep.cols + r, ep.cols, n, v);
         }
-        act32(p.act, v);
+    } else if (p.vec && n % 8 == 0) {
+        // every lane a piece of its own row, 16 bytes at a time
+        if (r < p.I) {
+            if (ep.bias) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            if (i >= n)
-                continue;
-            const int64_t row = c0 + i;
-            if (p.out_f32) {
-                if (ep.residual)
-                    v[i] += static_cast<const float *>(ep.residual)[row * ep.ldr + r];
-                static_cast<float *>(ep.out)[row * ep.ldo + r] = v[i];
-            } else {
-                if (ep.residual)
-                    v[i] += __bfloat162float(
-                        static_cast<const __nv_bfloat16 *>(ep.residual)[row * ep.ldr + r]);
-                static_cast<__nv_bfloat16 *>(ep.out)[row * ep.ldo + r] = __float2bfloat16_rn(v[i]);
+                for (int i = 0; i < 32; ++i)
+                    if (i < n)
+                        v[i] += __ldg(ep.bias + c0 + i);
             }
+            if (ep.preact)
+                store_run(ep.preact, r * ep.cols + c0, false, n, v);
+            act32(p.act, v);
+            if (ep.residual)
+                add_run(ep.residual, r * ep.ldr + c0, p.out_f32, n, v);
+            store_run(ep.out, r * ep.ldo + c0, p.out_f32, n, v);
+        }
+    } else {
+        // turned over: the lanes hold consecutive columns, whatever their alignment
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            st[i * kTurn + lane] = v[i];
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            v[i] = st[lane * kTurn + i];
+        __syncwarp();
+        if (lane < n) {
+            const float b = ep.bias ? __ldg(ep.bias + c0 + lane) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                v[i] += b;
+            const int rows = p.I - row0 < 32 ? static_cast<int>(p.I - row0) : 32;
+            const int64_t col = c0 + lane;
+            finish_run(p, row0 * ep.ldo + col, ep.ldo, row0 * ep.ldr + col, ep.ldr,
+                       row0 * ep.cols + col, ep.cols, rows, v);
         }
     }
 }
 
-__device__ __forceinline__ void epi_barrier()
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v)
 {
-    asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-template <int CG, bool P_MN, bool Q_MN>
+template <int CG, bool P_MN, bool Q_MN, bool SLICED>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_tc_kernel(const __grid_constant__ CUtensorMap tmP,
                      const __grid_constant__ CUtensorMap tmQ, const TcParams p)
@@ -241,7 +273,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * STAGE_BYTES);
+    float *turn = reinterpret_cast<float *>(smem + STAGES * STAGE_BYTES);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * STAGE_BYTES + TURN_BYTES);
     uint64_t *full = bars;
     uint64_t *empty = bars + STAGES;
     uint64_t *acc_full = bars + 2 * STAGES;
@@ -249,14 +282,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *drain = bars + 2 * STAGES + 4;
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bars + 2 * STAGES + 5);
     volatile int *s_abort = reinterpret_cast<volatile int *>(s_tmem + 1);
-    volatile uint32_t *s_last = reinterpret_cast<volatile uint32_t *>(s_tmem + 2);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
+    const uint32_t crank = CG == 2 || SLICED ? cluster_ctarank() : 0u;
+    const uint32_t rank = CG == 2 ? (crank & 1u) : 0u;       // in the pair
+    const uint32_t lead = crank - rank;                      // the pair's first CTA
     const bool leader = rank == 0;
-    const int worker = blockIdx.x / CG;
-    const int workers = gridDim.x / CG;
+    const int slice = SLICED ? static_cast<int>(crank) / CG : 0;
+    const int worker = blockIdx.x / (SLICED ? CG * p.slices : CG);
+    const int workers = gridDim.x / (SLICED ? CG * p.slices : CG);
+    const int kb_lo = SLICED ? static_cast<int>(static_cast<int64_t>(p.kblocks) * slice / p.slices) : 0;
+    const int kb_hi = SLICED ? static_cast<int>(static_cast<int64_t>(p.kblocks) * (slice + 1) / p.slices)
+                             : p.kblocks;
+    const int kb_half = SLICED ? (kb_lo + kb_hi + 1) / 2 : kb_hi;   // from here on in accumulator 1
     const int tj = CG == 2 ? 256 : p.bn;     // tile columns
 
     if (warp == 0 && lane == 0) {
@@ -291,14 +330,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem_base = *s_tmem;
     grid_dep_wait();
 
-    // unit u: slice u % splits of tile u / splits; consecutive tiles share their columns
-    auto unit_at = [&](int u, int &i0, int &j0, int &kb0, int &kb1) {
-        const int tile = u / p.splits, s = u - tile * p.splits;
-        const int jt = tile / p.i_tiles, it = tile - jt * p.i_tiles;
+    // consecutive tiles share their columns
+    auto tile_at = [&](int u, int &i0, int &j0) {
+        const int jt = u / p.i_tiles, it = u - jt * p.i_tiles;
         i0 = it * TI;
         j0 = jt * tj;
-        kb0 = static_cast<int>(static_cast<int64_t>(p.kblocks) * s / p.splits);
-        kb1 = static_cast<int>(static_cast<int64_t>(p.kblocks) * (s + 1) / p.splits);
     };
     auto wait = [&](uint64_t *bar, uint32_t parity, volatile int *abort) {
         return CG == 2 ? mbar_wait_bounded_cluster(bar, parity, abort)
@@ -312,12 +348,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t ph = 0, last_par = 0, used = 0;
             bool ok = true;
             const uint32_t bytes = CG * (A_BYTES + p.b_bytes);
-            for (int u = worker; u < p.units && ok; u += workers) {
-                int i0, j0, kb0, kb1;
-                unit_at(u, i0, j0, kb0, kb1);
+            for (int u = worker; u < p.tiles && ok; u += workers) {
+                int i0, j0;
+                tile_at(u, i0, j0);
                 i0 += static_cast<int>(rank) * 128;
                 j0 += static_cast<int>(rank) * 128;
-                for (int kb = kb0; kb < kb1; ++kb) {
+                for (int kb = kb_lo; kb < kb_hi; ++kb) {
                     if (!wait(&empty[s], ph ^ 1u, s_abort)) {
                         set_status(p.status, DEV_TIMEOUT_PRODUCER);
                         *s_abort = 1;
@@ -328,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint8_t *sb = sa + A_BYTES;
                     if (leader)
                         mbar_arrive_expect_tx(&full[s], bytes);
-                    const uint32_t pbar = CG == 2 ? mapa_shared(smem_u32(&full[s]), 0) : 0u;
+                    const uint32_t pbar = CG == 2 ? mapa_shared(smem_u32(&full[s]), lead) : 0u;
                     auto load = [&](uint8_t *dst, const CUtensorMap *m, int c0, int c1) {
                         if (CG == 2)
                             tma_load_2d_pairbar(dst, m, pbar, c0, c1);
@@ -373,9 +409,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t ph = 0;
             int it = 0;
             bool ok = true;
-            for (int u = worker; u < p.units && ok; u += workers, ++it) {
-                int i0, j0, kb0, kb1;
-                unit_at(u, i0, j0, kb0, kb1);
+            const uint16_t both = static_cast<uint16_t>(0x3u << lead);
+            for (int u = worker; u < p.tiles && ok; u += workers, ++it) {
                 const int a = it & 1;
                 const uint32_t aph = (it >> 1) & 1;
                 if (!wait(&acc_empty[a], aph ^ 1u, s_abort)) {
@@ -384,8 +419,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                const uint32_t d_tmem = tmem_base + a * ACC;
-                for (int kb = kb0; kb < kb1; ++kb) {
+                const uint32_t d_tmem = tmem_base + a * ACC;        // a = 0 in a slice
+                for (int kb = kb_lo; kb < kb_hi; ++kb) {
                     if (!wait(&full[s], ph, s_abort)) {
                         set_status(p.status, DEV_TIMEOUT_MMA);
                         *s_abort = 1;
@@ -401,14 +436,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                  : sdesc_kmajor_sw128(sa + kk * 32);
                         const uint64_t db = Q_MN ? sdesc_mnmajor_sw128(sb + kk * 2048)
                                                  : sdesc_kmajor_sw128(sb + kk * 32);
-                        const uint32_t add = (kb > kb0 || kk > 0) ? 1u : 0u;
+                        const bool second = SLICED && kb >= kb_half;
+                        const uint32_t d = second ? d_tmem + ACC : d_tmem;
+                        const uint32_t add = (kb > (second ? kb_half : kb_lo) || kk > 0) ? 1u : 0u;
                         if (CG == 2)
-                            tc_mma_bf16_pair(d_tmem, da, db, idesc, add);
+                            tc_mma_bf16_pair(d, da, db, idesc, add);
                         else
-                            tc_mma_bf16(d_tmem, da, db, idesc, add);
+                            tc_mma_bf16(d, da, db, idesc, add);
                     }
                     if (CG == 2)
-                        tc_commit_pair_mc(&empty[s], 0x3);
+                        tc_commit_pair_mc(&empty[s], both);
                     else
                         tc_commit(&empty[s]);
                     if (++s == STAGES) {
@@ -418,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (ok) {
                     if (CG == 2)
-                        tc_commit_pair_mc(&acc_full[a], 0x3);
+                        tc_commit_pair_mc(&acc_full[a], both);
                     else
                         tc_commit(&acc_full[a]);
                 }
@@ -428,108 +465,119 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ================= epilogue (this CTA's 128 rows) =================
         const int q = warp & 3;                  // TMEM lanes of this warp
         const int half = (warp - 2) >> 2;
-        const int r_local = q * 32 + lane;
-        const uint32_t leader_empty[2] = {
-            CG == 2 ? mapa_shared(smem_u32(&acc_empty[0]), 0) : 0u,
-            CG == 2 ? mapa_shared(smem_u32(&acc_empty[1]), 0) : 0u};
+        float *st = turn + (warp - 2) * 32 * kTurn;
+        const uint32_t lead_empty[2] = {
+            CG == 2 ? mapa_shared(smem_u32(&acc_empty[0]), lead) : 0u,
+            CG == 2 ? mapa_shared(smem_u32(&acc_empty[1]), lead) : 0u};
         int it = 0;
-        for (int u = worker; u < p.units; u += workers, ++it) {
-            int i0, j0, kb0, kb1;
-            unit_at(u, i0, j0, kb0, kb1);
+        for (int u = worker; u < p.tiles; u += workers, ++it) {
+            int i0, j0;
+            tile_at(u, i0, j0);
             const int a = it & 1;
             const uint32_t aph = (it >> 1) & 1;
-            bool got = wait(&acc_full[a], aph, s_abort);
-            got = __all_sync(0xffffffffu, got);
-            if (!got && lane == 0) {
-                set_status(p.status, DEV_TIMEOUT_EPILOGUE);
-                *s_abort = 1;
-            }
-            if (!got && p.splits == 1)
+            const bool got = wait(&acc_full[a], aph, s_abort);
+            if (!__all_sync(0xffffffffu, got)) {
+                if (lane == 0) {
+                    set_status(p.status, DEV_TIMEOUT_EPILOGUE);
+                    *s_abort = 1;
+                }
                 break;
+            }
+            if (SLICED)
+                break;                           // one tile; the slices meet below
             tc_fence_after();
             const uint32_t tacc = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + a * ACC;
-            const int64_t row = static_cast<int64_t>(i0) + rank * 128 + r_local;
-            if (p.splits == 1) {
+            const int64_t row0 = static_cast<int64_t>(i0) + rank * 128 + q * 32;
 #pragma unroll 1
-                for (int c = half * 32; c < tj; c += 64) {
-                    uint32_t v[32];
-                    float o[32];
-                    tmem_ld32(tacc + c, v);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        o[i] = __uint_as_float(v[i]);
-                    finish32(p, row, j0 + c, o);
-                }
-            } else {
-                // leave the partial tile; the last slice adds them up
-                float *mine = p.part + (static_cast<int64_t>(u) * CG + rank) * (ACC * 128);
-#pragma unroll 1
-                for (int c = half * 32; c < tj && got; c += 64) {
-                    uint32_t v[32];
-                    tmem_ld32(tacc + c, v);
-                    tmem_wait_ld();
-                    const int n = p.J - (j0 + c);        // columns that exist
-                    if (n >= 32) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            __stcg(mine + (c + i) * 128 + r_local, __uint_as_float(v[i]));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (i < n)
-                                __stcg(mine + (c + i) * 128 + r_local, __uint_as_float(v[i]));
-                    }
-                }
-                const int tile = u / p.splits;
-                __threadfence();
-                epi_barrier();
-                if (threadIdx.x == 64) {
-                    // every slice arrives, after a wait that gave up too, so the
-                    // ticket always comes back to 0
-                    *s_last = atomicInc(p.tickets + tile * CG + rank, p.splits - 1) ==
-                              static_cast<uint32_t>(p.splits - 1);
-                    __threadfence();
-                }
-                epi_barrier();
-                if (*s_last && got) {
-                    const float *first = p.part + (static_cast<int64_t>(tile) * p.splits * CG + rank) *
-                                                      (ACC * 128);
-#pragma unroll 1
-                    for (int c = half * 32; c < tj; c += 64) {
-                        float o[32];
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            o[i] = 0.0f;
-                        const int n = p.J - (j0 + c);
-                        const float *src = first + c * 128 + r_local;
-                        if (n >= 32) {
-                            for (int s = 0; s < p.splits; ++s, src += CG * (ACC * 128)) {
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    o[i] += __ldcg(src + i * 128);
-                            }
-                        } else {
-                            // few columns: the loads of the slices in flight together
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (i < n) {
-#pragma unroll 8
-                                    for (int s = 0; s < p.splits; ++s)
-                                        o[i] += __ldcg(src + i * 128 + s * (CG * (ACC * 128)));
-                                }
-                        }
-                        finish32(p, row, j0 + c, o);
-                    }
-                }
-                if (!got)
+            for (int c = half * 32; c < tj; c += 64) {
+                if (row0 >= p.I || j0 + c >= p.J)
                     break;
+                uint32_t v[32];
+                float o[32];
+                tmem_ld32(tacc + c, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    o[i] = __uint_as_float(v[i]);
+                finish_block(p, st, row0, j0 + c, 32, o);
             }
             tc_fence_before();
             if (CG == 2 && !leader)
-                mbar_arrive_cluster(leader_empty[a]);
+                mbar_arrive_cluster(lead_empty[a]);
             else
                 mbar_arrive(&acc_empty[a]);
+        }
+    }
+
+    if (SLICED) {
+        // ================= the slices' sums meet =================
+        // Every CTA of the cluster has finished its products, so the stages are
+        // free; CTA s of the CTAs with this pair rank takes columns [s w, s w + w).
+        // A CTA whose waits gave up takes part in the barriers all the same.
+        int i0, j0;
+        tile_at(worker, i0, j0);
+        const int w = p.share;
+        __syncwarp();
+        cluster_sync_all();
+        tc_fence_after();
+        const int q = warp & 3;
+        const int half = (warp - 2) >> 2;
+        const int r_local = q * 32 + lane;
+        const uint32_t recv = smem_u32(smem);    // [slice][w][128 rows] fp32
+        const int n = p.J - j0 < tj ? p.J - j0 : tj;
+        if (warp >= 2) {
+            const uint32_t tacc = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll 1
+            for (int c = half * 32; c < n; c += 64) {
+                uint32_t v[32], v2[32];
+                tmem_ld32(tacc + c, v);
+                tmem_ld32(tacc + ACC + c, v2);
+                tmem_wait_ld();
+                const bool two = kb_hi > kb_half;
+                int owner = c / w, at = c - owner * w;
+                uint32_t to = mapa_shared(recv + ((slice * w + at) * 128 + r_local) * 4,
+                                          owner * CG + rank);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    if (c + i < n)
+                        st_cluster_f32(to, __uint_as_float(v[i]) +
+                                               (two ? __uint_as_float(v2[i]) : 0.0f));
+                    to += 128 * 4;
+                    if (++at == w && c + i + 1 < n) {
+                        at = 0;
+                        ++owner;
+                        to = mapa_shared(recv + (slice * w * 128 + r_local) * 4, owner * CG + rank);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        cluster_sync_all();
+        if (warp >= 2) {
+            // this CTA's columns, half of them per warp of a row quarter
+            const float *sum = reinterpret_cast<const float *>(smem);
+            float *st = turn + (warp - 2) * 32 * kTurn;
+            const int wh = w / 2 < 32 ? w / 2 : 32;
+            const int64_t row0 = static_cast<int64_t>(i0) + rank * 128 + q * 32;
+            for (int c = half * wh; c < w; c += 2 * wh) {
+                const int col = slice * w + c;
+                if (col >= n || row0 >= p.I)
+                    break;
+                // the last share may reach past the tile's columns
+                int nc = w - c < wh ? w - c : wh;
+                nc = n - col < nc ? n - col : nc;
+                float o[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    o[i] = 0.0f;
+                for (int s = 0; s < p.slices; ++s) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (i < nc)
+                            o[i] += sum[(s * w + c + i) * 128 + r_local];
+                }
+                finish_block(p, st, row0, j0 + col, nc, o);
+            }
         }
     }
 
@@ -537,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (warp == 1 && lane == 0 && leader && *s_abort) {
         if (CG == 2)
-            tc_commit_pair_mc(drain, 0x1);
+            tc_commit_pair_mc(drain, static_cast<uint16_t>(1u << lead));
         else
             tc_commit(drain);
         volatile int never = 0;
@@ -589,6 +637,37 @@ bool make_map(CUtensorMap *m, const void *base, int64_t inner, int64_t outer, in
            CUDA_SUCCESS;
 }
 
+template <int CG, bool P_MN, bool Q_MN, bool SLICED>
+cudaError_t launch_tc(const TcParams &p, const CUtensorMap &mP, const CUtensorMap &mQ, int workers,
+                      cudaStream_t stream)
+{
+    static DeviceOnce once;
+    cudaError_t e = device_once(once, nullptr, [](int *) {
+        return cudaFuncSetAttribute(linear_tc_kernel<CG, P_MN, Q_MN, SLICED>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    });
+    if (e != cudaSuccess)
+        return e;
+    const unsigned cluster = CG * p.slices;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(cluster * static_cast<unsigned>(workers), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, linear_tc_kernel<CG, P_MN, Q_MN, SLICED>, mP, mQ, p);
+    count_launches(1);
+    return e;
+}
+
 template <int CG, bool P_MN, bool Q_MN>
 cudaError_t launch_tc(const TcParams &p, const void *P, int64_t ldp, const void *Q, int64_t ldq,
                       int64_t K, int workers, cudaStream_t stream)
@@ -599,105 +678,89 @@ cudaError_t launch_tc(const TcParams &p, const void *P, int64_t ldp, const void 
                           : make_map(&mQ, Q, K, p.J, ldq, CG == 2 ? 128 : p.bn));
     if (!ok)
         return cudaErrorInvalidValue;
-    static DeviceOnce once;
-    cudaError_t e = device_once(once, nullptr, [](int *) {
-        return cudaFuncSetAttribute(linear_tc_kernel<CG, P_MN, Q_MN>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-    });
-    if (e != cudaSuccess)
-        return e;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(CG * workers), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = SMEM_BYTES;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = CG == 2 ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, linear_tc_kernel<CG, P_MN, Q_MN>, mP, mQ, p);
-    count_launches(1);
-    return e;
+    return p.slices > 1 ? launch_tc<CG, P_MN, Q_MN, true>(p, mP, mQ, workers, stream)
+                        : launch_tc<CG, P_MN, Q_MN, false>(p, mP, mQ, workers, stream);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-}  // namespace
-
 // How a product is cut up; see the file's head.
-LinearPlan linear_plan(int64_t I, int64_t J, int64_t K, bool may_swap)
+struct Plan {
+    int cg;                  // CTAs per tile
+    bool swap;               // the transposed product
+    int bn;                  // tile columns
+    int slices;              // of k per tile
+    int64_t tiles;
+};
+
+Plan plan_of(int64_t I, int64_t J, int64_t K, bool may_swap, bool out_f32)
 {
     constexpr int kSms = 148;
-    LinearPlan pl{};
+    Plan pl{};
     const int64_t kb = ceil_div(K, BK);
     pl.swap = may_swap && I <= 64 && J > I;
     const int64_t rows = pl.swap ? J : I, cols = pl.swap ? I : J;
-    int64_t tiles;
     const int64_t pairs = ceil_div(rows, 256) * ceil_div(cols, 256);
     if (!pl.swap && rows > 128 && cols > 128 && (pairs >= kSms / 4 || kb * pairs >= kSms * 4)) {
         pl.cg = 2;
         pl.bn = 256;
-        tiles = pairs;
+        pl.tiles = pairs;
     } else {
         pl.cg = 1;
         pl.bn = static_cast<int>(cols >= 128 ? 128 : (cols + 15) / 16 * 16);
-        tiles = ceil_div(rows, 128) * ceil_div(cols, pl.bn);
+        pl.tiles = ceil_div(rows, 128) * ceil_div(cols, pl.bn);
     }
-    // idle SMs take slices of k, of at least 4 blocks of 64
-    int64_t s = kSms / (tiles * pl.cg);
-    if (s > kb / 4)
-        s = kb / 4;
-    pl.splits = static_cast<int>(s < 1 ? 1 : s);
-    pl.tiles = tiles;
+    // idle SMs take slices of k, of at least 2 blocks of 64, as long as all the
+    // clusters run at once: the GPU holds this many of each size (with one CTA
+    // per SM; not every SM has the neighbours that a cluster needs)
+    constexpr int kHeld[9] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
+    const int most = 8 / pl.cg;
+    pl.slices = 1;
+    for (int n = 2; n <= most; ++n)
+        if (pl.tiles <= kHeld[n * pl.cg] && kb >= n * 2)
+            pl.slices = n;
+    // fp32 results: chains of at most 1024 of k per accumulator (of two), as far as slices go
+    if (out_f32 && K > 1024)
+        while (pl.slices < most && (pl.slices == 1 || K > 2048 * pl.slices))
+            ++pl.slices;
     return pl;
 }
 
-size_t linear_plan_part_bytes(const LinearPlan &pl)
-{
-    return pl.splits > 1 ? static_cast<size_t>(pl.tiles) * pl.splits * pl.cg * (128 * pl.cg) * 128 * 4
-                         : 0;
-}
+}  // namespace
 
 cudaError_t launch_linear_tc(const LinearGemm &L, cudaStream_t stream)
 {
     int sms = 148, dev = 0;
     if (cudaGetDevice(&dev) == cudaSuccess)
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const LinearPlan pl = linear_plan(L.I, L.J, L.K, L.p_kmajor);
+    const Plan pl = plan_of(L.I, L.J, L.K, L.p_kmajor, L.out_f32);
     const bool sw = pl.swap;
     TcParams p{};
     p.I = static_cast<int32_t>(sw ? L.J : L.I);
     p.J = static_cast<int32_t>(sw ? L.I : L.J);
     p.i_tiles = static_cast<int32_t>(ceil_div(p.I, 128 * pl.cg));
-    p.j_tiles = static_cast<int32_t>(ceil_div(p.J, pl.bn));
-    p.splits = pl.splits;
-    const int64_t units = static_cast<int64_t>(p.i_tiles) * p.j_tiles * p.splits;
-    if (units > 0x7FFFFFFF)
+    if (pl.tiles * pl.cg * pl.slices > 0x7FFFFFFF)
         return cudaErrorInvalidValue;
-    p.units = static_cast<int32_t>(units);
+    p.tiles = static_cast<int32_t>(pl.tiles);
+    p.slices = pl.slices;
+    // shares in whole 16-byte pieces of a row, twice (two warps); transposed: of any size
+    const int unit = sw ? 2 : 16;
+    p.share = static_cast<int32_t>(ceil_div(ceil_div(pl.bn, pl.slices), unit) * unit);
     p.kblocks = static_cast<int32_t>(ceil_div(L.K, BK));
     const bool q_mn = sw ? !L.p_kmajor : !L.q_kmajor;
     const bool p_mn = sw ? !L.q_kmajor : !L.p_kmajor;
     p.bn = pl.bn;
-    if (q_mn && pl.cg == 1)
-        p.bn = pl.bn;
     p.b_bytes = pl.cg == 2 ? B_BYTES : (q_mn ? static_cast<int32_t>(ceil_div(p.bn, 64)) * 8192
                                              : p.bn * BK * 2);
     p.act = L.act;
     p.swap = sw;
     p.out_f32 = L.out_f32;
     const int os = L.out_f32 ? 4 : 2;
-    auto vec = [](const void *ptr, int64_t ld, int es) {
-        return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && (ld * es) % 16 == 0;
+    auto on16 = [](const void *ptr, int64_t row_bytes) {
+        return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && row_bytes % 16 == 0;
     };
-    p.out_vec = vec(L.out, L.ldo, os);
-    p.res_vec = vec(L.residual, L.ldr, os);
-    p.pre_vec = vec(L.preact, L.J, 2);
+    p.vec = on16(L.out, L.ldo * os) && (!L.residual || on16(L.residual, L.ldr * os)) &&
+            (!L.preact || on16(L.preact, L.J * 2ll));
     p.ep.out = L.out;
     p.ep.ldo = L.ldo;
     p.ep.bias = L.bias;
@@ -706,14 +769,12 @@ cudaError_t launch_linear_tc(const LinearGemm &L, cudaStream_t stream)
     p.ep.preact = L.preact;
     p.ep.rows = static_cast<int32_t>(L.I);
     p.ep.cols = L.J;
-    p.part = L.part;
-    p.tickets = L.tickets;
     p.status = L.status;
     const void *P = sw ? L.Q : L.P, *Q = sw ? L.P : L.Q;
     const int64_t ldp = sw ? L.ldq : L.ldp, ldq = sw ? L.ldp : L.ldq;
-    // slices: one unit per worker, so that a launch that gave up leaves no ticket behind
-    const int64_t cap = p.splits > 1 ? units : sms / pl.cg;
-    const int workers = static_cast<int>(units < cap ? units : cap);
+    // a cluster of slices takes one tile; without slices the CTAs (pairs) stay
+    const int64_t cap = pl.slices > 1 ? pl.tiles : sms / pl.cg;
+    const int workers = static_cast<int>(pl.tiles < cap ? pl.tiles : cap);
     if (pl.cg == 2) {
         if (p_mn)
             return q_mn ? launch_tc<2, true, true>(p, P, ldp, Q, ldq, L.K, workers, stream)

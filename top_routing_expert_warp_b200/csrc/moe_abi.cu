@@ -486,17 +486,15 @@ LinearLayout linear_layout(const moe_linear_config &c, bool backward)
     const int64_t es = elem_size(c.dtype);
     L.ldz = (c.n_out + 7) / 8 * 8;
     L.status = take(256);
-    if (c.M > 0) {
+    if (c.dtype == MOE_F32 && c.M > 0) {
         L.tickets = take(moe::kLinearMaxTickets * sizeof(uint32_t));
-        auto part = [&](int64_t I, int64_t J, int64_t K, bool swap) {
-            return c.dtype == MOE_BF16
-                       ? moe::linear_plan_part_bytes(moe::linear_plan(I, J, K, swap))
-                       : moe::simt_plan_part_bytes(moe::simt_plan(I, J, K));
+        auto part = [&](int64_t I, int64_t J, int64_t K) {
+            return moe::simt_plan_part_bytes(moe::simt_plan(I, J, K));
         };
-        size_t most = part(c.M, c.n_out, c.n_in, true);
+        size_t most = part(c.M, c.n_out, c.n_in);
         if (backward) {
-            most = std::max(most, part(c.M, c.n_in, c.n_out, true));
-            most = std::max(most, part(c.n_out, c.n_in, c.M, false));
+            most = std::max(most, part(c.M, c.n_in, c.n_out));
+            most = std::max(most, part(c.n_out, c.n_in, c.M));
         }
         L.part = take(most);
     }
