@@ -98,6 +98,7 @@ struct SimtParams {
     int64_t ldp, ldq;
     int64_t I, K;
     int32_t J, i_tiles, splits, act;
+    int32_t vec;             // output rows start on 16-byte boundaries
     lin::Epilogue ep;
     float *part;             // [units][64][64]
     uint32_t *tickets;       // [tiles], zero between launches
@@ -112,6 +113,16 @@ __device__ __forceinline__ float act_any(int act, float z)
     case MOE_LINEAR_GELU_TANH: return lin::act_fwd<MOE_LINEAR_GELU_TANH>(z);
     default: return z;
     }
+}
+
+template <int ACT>
+__device__ __forceinline__ void act_all(float (&v)[8][4])
+{
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+            v[x][y] = lin::act_fwd<ACT>(v[x][y]);
 }
 
 // A 64 x 64 tile (or a slice of its k range) per block, 8 x 4 outputs per
@@ -213,27 +224,59 @@ __global__ void __launch_bounds__(kGemmThreads) linear_simt_kernel(const __grid_
             }
         }
     }
+    // step by step over all 32 outputs, so that a step's branch is taken once
     const lin::Epilogue &ep = p.ep;
-#pragma unroll
-    for (int x = 0; x < 8; ++x) {
-        const int64_t row = i0 + ti + x;
-        if (row >= p.I)
-            continue;
+    const int64_t row0 = i0 + ti, col = j0 + tj;
+    const int rows = p.I - row0 < 8 ? static_cast<int>(p.I - row0) : 8;
+    const int n = p.J - col < 4 ? static_cast<int>(p.J - col) : 4;
+    if (ep.bias) {
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-            const int64_t col = j0 + tj + y;
-            if (col >= p.J)
-                continue;
-            float z = out[x][y];
-            if (ep.bias)
-                z += __ldg(ep.bias + col);
-            if (ep.preact)
-                static_cast<float *>(ep.preact)[row * ep.cols + col] = z;
-            z = act_any(p.act, z);
-            if (ep.residual)
-                z += static_cast<const float *>(ep.residual)[row * ep.ldr + col];
-            static_cast<float *>(ep.out)[row * ep.ldo + col] = z;
+            const float b = y < n ? __ldg(ep.bias + col + y) : 0.0f;
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+                out[x][y] += b;
         }
+    }
+    if (ep.preact) {
+        float *z = static_cast<float *>(ep.preact) + row0 * ep.cols + col;
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                if (x < rows && y < n)
+                    z[x * static_cast<int64_t>(ep.cols) + y] = out[x][y];
+    }
+    switch (p.act) {
+    case MOE_LINEAR_RELU: act_all<MOE_LINEAR_RELU>(out); break;
+    case MOE_LINEAR_SILU: act_all<MOE_LINEAR_SILU>(out); break;
+    case MOE_LINEAR_GELU: act_all<MOE_LINEAR_GELU>(out); break;
+    case MOE_LINEAR_GELU_TANH: act_all<MOE_LINEAR_GELU_TANH>(out); break;
+    default: break;
+    }
+    if (ep.residual) {
+        const float *r = static_cast<const float *>(ep.residual) + row0 * ep.ldr + col;
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                if (x < rows && y < n)
+                    out[x][y] += r[x * ep.ldr + y];
+    }
+    float *o = static_cast<float *>(ep.out) + row0 * ep.ldo + col;
+    if (p.vec && n == 4) {
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+            if (x < rows)
+                *reinterpret_cast<float4 *>(o + x * ep.ldo) =
+                    make_float4(out[x][0], out[x][1], out[x][2], out[x][3]);
+    } else {
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                if (x < rows && y < n)
+                    o[x * ep.ldo + y] = out[x][y];
     }
 }
 
@@ -486,9 +529,9 @@ lin::Epilogue epilogue_of(const LinearGemm &L)
 template <typename T, typename TO>
 void run_rows(const LinearGemm &L, cudaStream_t stream)
 {
-    // warps per output so that at least 24 warps run on each SM
+    // warps per output so that at least 40 warps run on each SM
     int wpr = 1;
-    while (wpr < 8 && static_cast<int64_t>(L.J) * wpr < 148 * 24)
+    while (wpr < 8 && static_cast<int64_t>(L.J) * wpr < 148 * 40)
         wpr *= 2;
     const int per = kThreads / 32 / wpr;
     auto kernel = L.I == 1 ? linear_rows_kernel<T, TO, 1>
@@ -559,6 +602,7 @@ cudaError_t launch_linear_simt(const LinearGemm &L, cudaStream_t stream)
     p.i_tiles = static_cast<int32_t>((L.I + TM - 1) / TM);
     p.splits = pl.splits;
     p.act = L.act;
+    p.vec = reinterpret_cast<uintptr_t>(L.out) % 16 == 0 && L.ldo % 4 == 0;
     p.ep = epilogue_of(L);
     p.part = L.part;
     p.tickets = L.tickets;

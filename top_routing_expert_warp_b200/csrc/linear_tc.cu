@@ -719,9 +719,9 @@ Plan plan_of(int64_t I, int64_t J, int64_t K, bool may_swap, bool out_f32)
     for (int n = 2; n <= most; ++n)
         if (pl.tiles <= kHeld[n * pl.cg] && kb >= n * 2)
             pl.slices = n;
-    // fp32 results: chains of at most 1024 of k per accumulator (of two), as far as slices go
+    // fp32 results: chains of at most 1280 of k per accumulator (of two), as far as slices go
     if (out_f32 && K > 1024)
-        while (pl.slices < most && (pl.slices == 1 || K > 2048 * pl.slices))
+        while (pl.slices < most && (pl.slices == 1 || K > 2560 * pl.slices))
             ++pl.slices;
     return pl;
 }

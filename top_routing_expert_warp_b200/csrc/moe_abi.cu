@@ -515,7 +515,7 @@ void linear_scratch(moe::LinearGemm *G, uint8_t *ws, const LinearLayout &L)
 
 cudaError_t launch_linear(const moe::LinearGemm &G, cudaStream_t s)
 {
-    if (G.I <= moe::kLinearRowsMax && G.p_kmajor && G.q_kmajor)
+    if (G.I <= (G.dtype == MOE_BF16 ? moe::kLinearRowsMaxBf16 : moe::kLinearRowsMaxF32) && G.p_kmajor && G.q_kmajor)
         return moe::launch_linear_rows(G, s);
     return G.dtype == MOE_BF16 ? moe::launch_linear_tc(G, s) : moe::launch_linear_simt(G, s);
 }
