@@ -73,18 +73,39 @@ __device__ __forceinline__ float slot_max(float v)
     return v;
 }
 
-// Bits that order as the values do (no NaN; -0 as +0), all above 1: key 0
-// marks what cannot be chosen, key 1 an expert that is switched off.
+// Bits that order as the values do (no NaN; -0 as +0), all above 0: key 0
+// marks what cannot be chosen; an expert that is switched off counts -inf.
 __device__ __forceinline__ uint64_t order_key(double v)
 {
-    const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v + 0.0));
-    return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
+    const int64_t b = __double_as_longlong(v + 0.0);
+    return static_cast<uint64_t>(b ^ ((b >> 63) | static_cast<int64_t>(0x8000000000000000ull)));
 }
 
 __device__ __forceinline__ uint32_t order_key(float v)
 {
-    const uint32_t b = __float_as_uint(v + 0.0f);
-    return (b >> 31) ? ~b : (b | 0x80000000u);
+    const int32_t b = __float_as_int(v + 0.0f);
+    return static_cast<uint32_t>(b ^ ((b >> 31) | static_cast<int32_t>(0x80000000u)));
+}
+
+constexpr uint32_t kOffKey = 0x007FFFFFu;     // of -inf
+
+// e^x in 32 bits within 4 half steps, x at most 88: 2^t with t = x log2(e)
+// rounded, then corrected by the rounding of t.  Below 2^-126 (-inf too): 0.
+__device__ __forceinline__ float exp_32(float x)
+{
+    x = fmaxf(x, -120.0f);
+    const float t = x * 1.44269504f;
+    const float lo = fmaf(x, 1.44269504f, -t);
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    return fmaf(e * 0.693147181f, lo, e);
+}
+
+__device__ __forceinline__ float recip_32(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
 __device__ __forceinline__ float key_value(uint32_t k)
@@ -186,14 +207,19 @@ __device__ __forceinline__ double recip_64(double x)
 __device__ __forceinline__ uint32_t key_max(uint32_t v) { return __reduce_max_sync(kAll, v); }
 __device__ __forceinline__ uint64_t key_max(uint64_t v) { return warp_key_max(v); }
 
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ float smaller(float a, float b) { return fminf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return a > b ? a : b; }
+__device__ __forceinline__ double smaller(double a, double b) { return a > b ? b : a; }
+
 // Inserts v into a list of the M largest values, largest first.
 template <int M, typename F>
 __device__ __forceinline__ void list_insert(F (&a)[M], F v)
 {
 #pragma unroll
     for (int i = 0; i < M; ++i) {
-        const F hi = v > a[i] ? v : a[i];
-        v = v > a[i] ? a[i] : v;
+        const F hi = larger(v, a[i]);
+        v = smaller(v, a[i]);
         a[i] = hi;
     }
 }
@@ -286,9 +312,7 @@ __device__ __forceinline__ bool choose(const RouteParams &p, const F (&v)[VPL],
     K key[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-        key[i] = e0 + i >= N ? K(0)
-                             : (v[i] == -INFINITY ? K(1)
-                                                  : order_key(p.bias ? v[i] : static_cast<F>(l[i])));
+        key[i] = e0 + i >= N ? K(0) : order_key(p.bias ? v[i] : static_cast<F>(l[i]));
     if (p.n_groups > 1) {
         const int nl = p.node_lanes, per = p.per_node;
         const int g = lane / nl;
@@ -336,17 +360,29 @@ __device__ __forceinline__ bool choose(const RouteParams &p, const F (&v)[VPL],
             __syncwarp();
         }
     }
-    // the best of each lane; the winner's lane looks again
-    K best = 0;
-    int bi = 0;
+    // the best two of each lane; a lane that won twice looks again
+    K best = 0, second = 0;
+    int bi = 0, si = 0;
+    if (rounds > 2) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-        if (key[i] > best) {
-            best = key[i];
-            bi = i;
+        for (int i = 0; i < VPL; ++i) {
+            const bool first = key[i] > best, other = key[i] > second;
+            second = first ? best : (other ? key[i] : second);
+            si = first ? bi : (other ? i : si);
+            best = first ? key[i] : best;
+            bi = first ? i : bi;
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                bi = i;
+            }
+    }
     my_key = 0;
     mine = 0;
+    uint32_t gone = 0;
     for (int j = 0; j < rounds; ++j) {
         const K m = key_max(best);
         const int src = __ffs(__ballot_sync(kAll, best == m)) - 1;
@@ -355,18 +391,20 @@ __device__ __forceinline__ bool choose(const RouteParams &p, const F (&v)[VPL],
             mine = e;
             my_key = m;
         }
-        if (lane == src && j + 1 < rounds) {
-            best = 0;
-            const int gone = bi;
+        if (j + 1 == rounds)
+            break;
+        const bool won = lane == src;
+        gone |= won ? 1u << bi : 0u;
+        best = won ? second : best;
+        bi = won ? si : bi;
+        second = won ? K(0) : second;
+        if (won && best == 0 && VPL > 1) {
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                if (i == gone)
-                    key[i] = 0;
-                if (key[i] > best) {
+            for (int i = 0; i < VPL; ++i)
+                if (!((gone >> i) & 1u) && key[i] > best) {
                     best = key[i];
                     bi = i;
                 }
-            }
         }
     }
     return near;
@@ -468,36 +506,48 @@ __global__ void __launch_bounds__(kThreads, VPL == 8 ? 3 : 4)
         load_logits<VPL, BF16>(row, e0, N, p.vec, nxt);
     for (; t < p.T; t += step, row += row_step, slot += step * k) {
         float l[VPL];
-        float mx = -INFINITY;
+        float mx = -INFINITY, all = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            l[i] = clean_logit(nxt[i], bad);
-            mx = fmaxf(mx, l[i]);
+            l[i] = nxt[i];
+            all += l[i];
         }
+        if (__any_sync(kAll, !(all < INFINITY))) {      // a NaN or +inf among them
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                l[i] = clean_logit(l[i], bad);
+        }
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            mx = fmaxf(mx, l[i]);
         if (t + step < p.T)
             load_logits<VPL, BF16>(row + row_step, e0, N, p.vec, nxt);
-        mx = warp_max(mx);
+        const bool scores = SOFTMAX || p.want_p || values;
+        if (scores || p.renorm)
+            mx = warp_max(mx);
         const float shift = mx == -INFINITY ? 0.0f : mx;
         const bool tiny = !SOFTMAX && mx < kTinyScore;
         // s, or up to a factor: e^{l - max} for a softmax and below kTinyScore
         float s[VPL], z = 0.0f;
-        if (SOFTMAX || tiny) {
+        float rz = 0.0f;
+        if (scores) {
+            if (SOFTMAX || tiny) {
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                s[i] = expf(l[i] - shift);
-                z += s[i];
-            }
-        } else {
+                for (int i = 0; i < VPL; ++i) {
+                    s[i] = exp_32(l[i] - shift);
+                    z += s[i];
+                }
+            } else {
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                s[i] = __fdividef(1.0f, 1.0f + expf(-l[i]));
-                z += s[i];
+                for (int i = 0; i < VPL; ++i) {
+                    s[i] = recip_32(1.0f + exp_32(fminf(-l[i], 80.0f)));
+                    z += s[i];
+                }
             }
         }
-        float rz = 0.0f;
         if (SOFTMAX || p.want_p) {
             z = warp_sum(z);
-            rz = z > 0.0f ? __fdividef(1.0f, z) : 0.0f;
+            rz = z > 0.0f ? recip_32(z) : 0.0f;
 #pragma unroll
             for (int i = 0; i < VPL; ++i) {
                 const float q = s[i] * rz;
@@ -523,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, VPL == 8 ? 3 : 4)
             for (int i = 0; i < VPL; ++i)
                 s[i] = l[i];
             choose<float, uint32_t, VPL>(p, s, l, nullptr, 0.0f, k, mine, won);
-            if (lane < k && won > 1u)
+            if (lane < k)
                 le = key_value(won);
         } else {
             bool exact = tiny;
@@ -539,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, VPL == 8 ? 3 : 4)
                     // each slot against the next one, the last against the first left out
                     const uint32_t nk = __shfl_down_sync(kAll, won, 1);
                     const int ne = __shfl_down_sync(kAll, mine, 1);
-                    bool close = lane < k && nk > 1u && !(key_value(won) - key_value(nk) > margin);
+                    bool close = lane < k && nk > kOffKey && !(key_value(won) - key_value(nk) > margin);
                     if (close)
                         // equal logits with equal biases are equal in every precision
                         close = won != nk || load_logit<BF16>(row, mine) != load_logit<BF16>(row, ne) ||
@@ -587,6 +637,29 @@ __global__ void __launch_bounds__(kThreads, VPL == 8 ? 3 : 4)
                 p.p_part[static_cast<int64_t>(blockIdx.x) * N + e] = sum;
         }
     }
+}
+
+// p_mean from the blocks' sums: 32 experts per block, every 32nd row per warp,
+// the warps' sums added in a fixed order.
+__global__ void __launch_bounds__(1024)
+    route_mean_kernel(const double *__restrict__ p_part, int rows, int N, int64_t T,
+                      float *__restrict__ p_mean)
+{
+    grid_dep_wait();
+    __shared__ double s_sum[32][33];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int e = blockIdx.x * 32 + lane;
+    double sum = 0.0;
+    if (e < N) {
+#pragma unroll 8
+        for (int r = warp; r < rows; r += 32)
+            sum += p_part[static_cast<int64_t>(r) * N + e];
+    }
+    s_sum[warp][lane] = sum;
+    __syncthreads();
+    sum = warp_sum(s_sum[lane][warp]);          // expert `warp` of the block
+    if (lane == 0 && blockIdx.x * 32 + warp < N)
+        p_mean[blockIdx.x * 32 + warp] = static_cast<float>(sum / static_cast<double>(T));
 }
 
 struct RouteGradParams {
@@ -641,8 +714,8 @@ __device__ __forceinline__ void store_logits(void *row, int e0, int N, bool vec,
 // s and 1 - s of the logistic function, both without cancellation.
 __device__ __forceinline__ void logistic(float l, float &s, float &om)
 {
-    const float t = expf(-fabsf(l));
-    const float r = __fdividef(1.0f, 1.0f + t);
+    const float t = exp_32(-fabsf(l));
+    const float r = recip_32(1.0f + t);
     const float tr = t * r;
     s = l > 0.0f ? r : tr;
     om = l > 0.0f ? tr : r;
@@ -706,12 +779,20 @@ __global__ void __launch_bounds__(kThreads, 4)
                     cm = p.dp_mean[me] * inv_t;
             }
         }
-        float l[VPL], mx = -INFINITY;
+        float l[VPL], mx = -INFINITY, all = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            l[i] = clean_logit(nxt[i], nan);
-            mx = fmaxf(mx, l[i]);
+            l[i] = nxt[i];
+            all += l[i];
         }
+        if (__any_sync(kAll, !(all < INFINITY))) {      // a NaN or +inf among them
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                l[i] = clean_logit(l[i], nan);
+        }
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            mx = fmaxf(mx, l[i]);
         slot += slot_step;
         if (t + step < p.T) {
             load_logits<VPL, BF16>(row + row_step, e0, N, p.vec, nxt);
@@ -729,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 4)
 #pragma unroll
             for (int i = 0; i < VPL; ++i) {
                 om[i] = 1.0f;
-                s[i] = expf(l[i] - shift);
+                s[i] = exp_32(l[i] - shift);
             }
         } else {
 #pragma unroll
@@ -887,7 +968,10 @@ cudaError_t launch_route(const RouteLaunch &L, cudaStream_t stream)
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !p.p_part)
         return e;
-    return launch_p_finalize(L.p_part, grid, L.N, L.T, L.p_mean, stream);
+    launch_k(route_mean_kernel, dim3((L.N + 31) / 32), dim3(1024), 0, stream, L.p_part, grid, L.N,
+             L.T, L.p_mean);
+    count_launches(1);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_route_grad(const RouteGradLaunch &L, cudaStream_t stream)
