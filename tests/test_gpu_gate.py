@@ -67,6 +67,10 @@ GATES = {
                                n_groups=4, topk_groups=2, group_top=3),
     "odd-nodes": dict(N=60, k=5, score="sigmoid", bias=0.2, renorm=False, scale=1.0,
                       n_groups=12, topk_groups=2, group_top=5),
+    "deep-nodes": dict(N=240, k=8, score="softmax", bias=0.02, renorm=True, scale=1.0,
+                       n_groups=3, topk_groups=1, group_top=60),
+    "exact-fit": dict(N=64, k=8, score="sigmoid", bias=0.1, renorm=True, scale=1.0,
+                      n_groups=16, topk_groups=2, group_top=4),      # as many experts as slots
     "top1": dict(N=128, k=1, score="softmax", bias=None, renorm=False, scale=1.0),
     "odd": dict(N=61, k=7, score="sigmoid", bias=0.1, renorm=True, scale=1.0),
     "few": dict(N=3, k=3, score="softmax", bias=1.0, renorm=True, scale=0.5),
@@ -101,6 +105,8 @@ def test_route_ties_and_near_ties(score, bias, nodes):
     base = torch.full((32, N), 0.75)
     step = torch.stack([torch.randperm(N, generator=g) for _ in range(32)]).float()
     l[32:] = base + step * 2.0 ** -24
+    # and a few of them near one another among others that are not
+    l[48:, 5:] = torch.randn(16, N - 5, generator=g)
     b = None
     if bias:
         b = torch.zeros(N)

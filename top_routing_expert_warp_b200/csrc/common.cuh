@@ -49,6 +49,14 @@ __device__ __forceinline__ void grid_dep_wait()
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// Lets the next kernel on the stream be scheduled before this one ends (once
+// every block has said so): its blocks set themselves up and wait in
+// grid_dep_wait, which still waits for this kernel's end.
+__device__ __forceinline__ void grid_dep_launch()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ------------------------------------------------------------------ smem
 __device__ __forceinline__ uint32_t smem_u32(const void *p)
 {

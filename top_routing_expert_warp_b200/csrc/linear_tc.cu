@@ -329,6 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem_base = *s_tmem;
     grid_dep_wait();
+    grid_dep_launch();
 
     // consecutive tiles share their columns
     auto tile_at = [&](int u, int &i0, int &j0) {

@@ -297,13 +297,14 @@ __device__ __forceinline__ double key_value_of(uint64_t k)
 }
 
 // The choice: v = s + b of this lane's experts (-inf: switched off), K the key
-// type of F.  Lane j < k gets its slot's expert in `mine`, lane j <= rounds - 1
-// the key it won with in `my_key`.  Returns whether a chosen node's score is
-// within node_margin of the first one left out.
+// type of F.  Lane j gets the j-th best expert in `mine` and its key in
+// `my_key`, for the `found` best: p.k of them, or with `margin` >= 0 one more,
+// and all (up to 32) that are not more than margin below the k-th.  Returns
+// whether a chosen node's score is within node_margin of the first one left out.
 template <typename F, typename K, int VPL>
 __device__ __forceinline__ bool choose(const RouteParams &p, const F (&v)[VPL],
-                                       const float (&l)[VPL], F *scratch, F node_margin,
-                                       int rounds, int &mine, K &my_key)
+                                       const float (&l)[VPL], F *scratch, F node_margin, F margin,
+                                       int &found, int &mine, K &my_key)
 {
     const int lane = threadIdx.x & 31;
     const int e0 = lane * VPL;
@@ -314,11 +315,14 @@ __device__ __forceinline__ bool choose(const RouteParams &p, const F (&v)[VPL],
     for (int i = 0; i < VPL; ++i)
         key[i] = e0 + i >= N ? K(0) : order_key(p.bias ? v[i] : static_cast<F>(l[i]));
     if (p.n_groups > 1) {
-        const int nl = p.node_lanes, per = p.per_node;
+        // (the 64-bit choice is rare: it takes the short way through scratch)
+        constexpr bool kWide = sizeof(F) == 8;
+        const int nl = kWide ? 1 : p.node_lanes, per = p.per_node;
+        const bool direct = !kWide && p.node_direct;
         const int g = lane / nl;
         const F *s_node = nullptr;
         int count = 0;
-        if (!p.node_direct) {
+        if (!direct) {
 #pragma unroll
             for (int i = 0; i < VPL; ++i)
                 scratch[e0 + i] = v[i];
@@ -328,13 +332,13 @@ __device__ __forceinline__ bool choose(const RouteParams &p, const F (&v)[VPL],
             count = g < p.n_groups ? (per - at + nl - 1) / nl : 0;
         }
         F sum;
-        if (p.group_top <= 2)
-            sum = node_sum<2, VPL, F>(v, s_node, count, nl, p.group_top);
-        else if (p.group_top <= 4)
-            sum = node_sum<4, VPL, F>(v, s_node, count, nl, p.group_top);
-        else
+        if (kWide || p.group_top > 4)
             sum = node_sum_any<F>(scratch + (g < p.n_groups ? g * per : 0),
                                   g < p.n_groups ? per : 0, p.group_top);
+        else if (p.group_top <= 2)
+            sum = node_sum<2, VPL, F>(v, s_node, count, nl, p.group_top);
+        else
+            sum = node_sum<4, VPL, F>(v, s_node, count, nl, p.group_top);
         K gkey = g < p.n_groups && lane == g * nl ? order_key(sum) : K(0);
         uint32_t chosen = 0;
         K m = 0;
@@ -346,7 +350,7 @@ __device__ __forceinline__ bool choose(const RouteParams &p, const F (&v)[VPL],
                 gkey = 0;
         }
         near = !(key_value_of(m) - key_value_of(key_max(gkey)) > node_margin);
-        if (p.node_direct) {
+        if (direct) {
             if (!((chosen >> g) & 1u)) {
 #pragma unroll
                 for (int i = 0; i < VPL; ++i)
@@ -363,7 +367,7 @@ __device__ __forceinline__ bool choose(const RouteParams &p, const F (&v)[VPL],
     // the best two of each lane; a lane that won twice looks again
     K best = 0, second = 0;
     int bi = 0, si = 0;
-    if (rounds > 2) {
+    if (p.k > 1) {
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
             const bool first = key[i] > best, other = key[i] > second;
@@ -382,16 +386,25 @@ __device__ __forceinline__ bool choose(const RouteParams &p, const F (&v)[VPL],
     }
     my_key = 0;
     mine = 0;
+    K kth = 0;
     uint32_t gone = 0;
-    for (int j = 0; j < rounds; ++j) {
+    for (found = 0; found < 32;) {
         const K m = key_max(best);
+        if (m == 0)
+            break;                   // no expert left (p.k of them there always are)
         const int src = __ffs(__ballot_sync(kAll, best == m)) - 1;
         const int e = __shfl_sync(kAll, e0 + bi, src);
-        if (lane == j) {
+        if (lane == found) {
             mine = e;
             my_key = m;
         }
-        if (j + 1 == rounds)
+        ++found;
+        if (found == p.k) {
+            kth = m;
+            if (margin < 0)
+                break;
+        }
+        if (found > p.k && !(key_value_of(kth) - key_value_of(m) <= margin))
             break;
         const bool won = lane == src;
         gone |= won ? 1u << bi : 0u;
@@ -427,35 +440,74 @@ __device__ __noinline__ int choose_exact(const RouteParams &p, const void *row, 
         mx = fmaxf(mx, l[i]);
     }
     mx = warp_max(mx);
-    double s[VPL], z = 0.0;
+    // one expert after another through s_val: this runs for a token in hundreds
+    // or thousands, whose warp then waits for its instructions most of all
+    double z = 0.0;
 #pragma unroll
+    for (int i = 0; i < VPL; ++i)
+        s_val[e0 + i] = l[i];
+#pragma unroll 1
     for (int i = 0; i < VPL; ++i) {
-        const double li = l[i];
+        const double li = s_val[e0 + i];
+        double si;
         if (SOFTMAX) {
-            s[i] = l[i] == -INFINITY ? 0.0 : exp_64(li - static_cast<double>(mx));
-            z += s[i];
+            si = exp_64(li - static_cast<double>(mx));
+            si = li == -INFINITY ? 0.0 : si;
+            z += si;
         } else {
             const double t = exp_64(-fabs(li));
             const double r = recip_64(1.0 + t);
-            s[i] = l[i] > 0.0f ? r : t * r;
+            si = li > 0.0 ? r : t * r;
         }
+        s_val[e0 + i] = si;
     }
     if (SOFTMAX) {
         z = warp_sum(z);
         z = z > 0.0 ? 1.0 / z : 0.0;
     }
+    double s[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         float b = (p.bias && e0 + i < p.N) ? p.bias[e0 + i] : 0.0f;
         b = fmaxf(b, -INFINITY);
-        if (SOFTMAX)
-            s[i] *= z;
+        s[i] = SOFTMAX ? s_val[e0 + i] * z : s_val[e0 + i];
         s[i] = l[i] == -INFINITY || b == -INFINITY ? -INFINITY : s[i] + static_cast<double>(b);
     }
-    int mine;
+    int mine, found;
     uint64_t won;
-    choose<double, uint64_t, VPL>(p, s, l, s_val, 0.0, p.k, mine, won);
+    choose<double, uint64_t, VPL>(p, s, l, s_val, 0.0, -1.0, found, mine, won);
     return mine;
+}
+
+// The `n` experts of lanes 0 .. n - 1 in the order of their 64-bit values,
+// logistic scores with a bias.
+template <bool BF16>
+__device__ __noinline__ int order_exact(const RouteParams &p, const void *row, int mine, int n)
+{
+    const int lane = threadIdx.x & 31;
+    bool ignore = false;
+    double v = -INFINITY;
+    if (lane < n) {
+        const float l = clean_logit(load_logit<BF16>(row, mine), ignore);
+        const float b = fmaxf(p.bias[mine], -INFINITY);
+        const double t = exp_64(-fabs(static_cast<double>(l)));
+        const double r = recip_64(1.0 + t);
+        if (l != -INFINITY && b != -INFINITY)
+            v = (l > 0.0f ? r : t * r) + static_cast<double>(b);
+    }
+    int rank = 0;
+    for (int j = 0; j < n; ++j) {
+        const double vj = __shfl_sync(kAll, v, j);
+        const int ej = __shfl_sync(kAll, mine, j);
+        rank += vj > v || (vj == v && ej < mine) ? 1 : 0;
+    }
+    int sorted = mine;
+    for (int j = 0; j < n; ++j) {
+        const int rj = __shfl_sync(kAll, rank, j);
+        const int ej = __shfl_sync(kAll, mine, j);
+        sorted = rj == lane ? ej : sorted;
+    }
+    return sorted;
 }
 
 // One warp per token, VPL consecutive experts per lane.  What bounds it is the
@@ -469,6 +521,7 @@ __global__ void __launch_bounds__(kThreads, VPL == 8 ? 3 : 4)
     route_kernel(const __grid_constant__ RouteParams p)
 {
     grid_dep_wait();
+    grid_dep_launch();
     __shared__ double s_val[kWarps][32 * VPL];   // scratch of a token's choice
     __shared__ double s_acc[kWarps][32 * VPL];   // sums of s / sum s, each lane its own
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -489,11 +542,12 @@ __global__ void __launch_bounds__(kThreads, VPL == 8 ? 3 : 4)
         s_acc[warp][e0 + i] = 0.0;
         part[i] = 0.0f;
     }
-    // Scores are at most 1 and their 32-bit values within 2^-21 of them (an
-    // exponential and a quotient, each off by a few half steps; a softmax's sum
-    // of up to 256 positive terms); adding the bias is off by 2^-24 of 1 + |b|.
-    // Values more than twice that apart, rounded up, are ordered right.
-    const float margin = 0x1p-19f * (1.0f + warp_max(bmax));
+    // Half steps of 32 bits (2^-24) that a value s + b may be off: a logistic
+    // score 3.1 (4 of the exponential times 1 - s, 3 of sum and reciprocal), a
+    // softmax's share 22 (its exponential, a sum of up to 256 terms, reciprocal
+    // and product), the addition 1 + |b|.  Values further apart than twice that
+    // are ordered right.
+    const float margin = (SOFTMAX ? 0x1p-18f : 0x1p-20f) * (1.0f + warp_max(bmax));
     const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
     const int64_t row_bytes = p.ld * (BF16 ? 2 : 4);
     const int64_t row_step = step * row_bytes;
@@ -564,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, VPL == 8 ? 3 : 4)
                 part[i] = 0.0f;
             }
         }
-        int mine;
+        int mine, found;
         uint32_t won;
         float le = -INFINITY;
         if (!values) {
@@ -572,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, VPL == 8 ? 3 : 4)
 #pragma unroll
             for (int i = 0; i < VPL; ++i)
                 s[i] = l[i];
-            choose<float, uint32_t, VPL>(p, s, l, nullptr, 0.0f, k, mine, won);
+            choose<float, uint32_t, VPL>(p, s, l, nullptr, 0.0f, -1.0f, found, mine, won);
             if (lane < k)
                 le = key_value(won);
         } else {
@@ -581,20 +635,30 @@ __global__ void __launch_bounds__(kThreads, VPL == 8 ? 3 : 4)
 #pragma unroll
                 for (int i = 0; i < VPL; ++i)
                     s[i] = l[i] == -INFINITY ? -INFINITY : s[i] + b[i];
-                // the sums of up to group_top values are off by that many times as much
+                // sums of group_top values are off by that many times as much, and by
+                // half a step of every partial sum
+                const float gt = static_cast<float>(p.group_top);
                 exact = choose<float, uint32_t, VPL>(p, s, l, reinterpret_cast<float *>(s_val[warp]),
-                                                     margin * static_cast<float>(p.group_top),
-                                                     p.bias && k < N ? k + 1 : k, mine, won);
+                                                     margin * gt * (1.0f + 0.125f * gt),
+                                                     p.bias && k < N ? margin : -1.0f, found, mine, won);
                 if (p.bias && !exact) {
-                    // each slot against the next one, the last against the first left out
+                    // each of the found experts against the next one
                     const uint32_t nk = __shfl_down_sync(kAll, won, 1);
                     const int ne = __shfl_down_sync(kAll, mine, 1);
-                    bool close = lane < k && nk > kOffKey && !(key_value(won) - key_value(nk) > margin);
+                    bool close = lane + 1 < found && nk > kOffKey &&
+                                 !(key_value(won) - key_value(nk) > margin);
                     if (close)
                         // equal logits with equal biases are equal in every precision
                         close = won != nk || load_logit<BF16>(row, mine) != load_logit<BF16>(row, ne) ||
                                 p.bias[mine] != p.bias[ne];
-                    exact = __any_sync(kAll, close);
+                    if (__any_sync(kAll, close)) {
+                        // the k best are among the found ones, unless those are 32 or
+                        // the shares' sum is not known well enough
+                        if (!SOFTMAX && found < 32)
+                            mine = order_exact<BF16>(p, row, mine, found);
+                        else
+                            exact = true;
+                    }
                 }
             }
             if (exact)
@@ -646,6 +710,7 @@ __global__ void __launch_bounds__(1024)
                       float *__restrict__ p_mean)
 {
     grid_dep_wait();
+    grid_dep_launch();
     __shared__ double s_sum[32][33];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int e = blockIdx.x * 32 + lane;
@@ -736,6 +801,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     route_grad_kernel(const __grid_constant__ RouteGradParams p)
 {
     grid_dep_wait();
+    grid_dep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int N = p.N, k = p.k;
     const int e0 = lane * VPL;
