@@ -43,7 +43,6 @@ __global__ void __launch_bounds__(kThreads)
                         int64_t rows_cap, uint32_t *status)
 {
     grid_dep_wait();
-    grid_dep_launch();
     __shared__ float s_dot[kThreads / 32][KM];
     constexpr int V = BF16 ? 8 : 4;
     constexpr int esz = BF16 ? 2 : 4;

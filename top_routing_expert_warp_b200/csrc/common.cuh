@@ -424,6 +424,26 @@ __device__ __forceinline__ float bf16_bits_to_f32(uint32_t bits16)
     return __uint_as_float(bits16 << 16);
 }
 
+// ------------------------------------------------------------------ math
+// e^x in 32 bits within 4 half steps, x at most 88: 2^t with t = x log2(e)
+// rounded, then corrected by the rounding of t.  Below 2^-126 (-inf too): 0.
+__device__ __forceinline__ float exp_32(float x)
+{
+    x = fmaxf(x, -120.0f);
+    const float t = x * 1.44269504f;
+    const float lo = fmaf(x, 1.44269504f, -t);
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    return fmaf(e * 0.693147181f, lo, e);
+}
+
+__device__ __forceinline__ float recip_32(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // ------------------------------------------------------------------ cp.async
 // 16-byte copy global -> shared; src_bytes = 0 reads nothing and fills zeros.
 __device__ __forceinline__ void cp_async_16(uint32_t smem_dst, const void *src, uint32_t src_bytes)

@@ -136,7 +136,6 @@ template <bool P_K, bool Q_K>
 __global__ void __launch_bounds__(kGemmThreads) linear_simt_kernel(const __grid_constant__ SimtParams p)
 {
     grid_dep_wait();
-    grid_dep_launch();
     __shared__ __align__(16) float s_p[2][TK][TM + kPad];
     __shared__ __align__(16) float s_q[2][TK][TN + kPad];
     __shared__ uint32_t s_last;
@@ -291,7 +290,6 @@ __global__ void __launch_bounds__(kThreads)
                        int N, int wpr, int act, const __grid_constant__ lin::Epilogue ep)
 {
     grid_dep_wait();
-    grid_dep_launch();
     constexpr int V = 16 / sizeof(T);
     constexpr int U = 8;
     __shared__ float s_sum[kThreads / 32][MR];
@@ -443,7 +441,6 @@ __global__ void __launch_bounds__(kThreads)
                      int64_t rows_per_block)
 {
     grid_dep_wait();
-    grid_dep_launch();
     __shared__ float s_sum[kThreads / 32][32 * V];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int col = (blockIdx.x * 32 + lane) * V;
@@ -495,7 +492,6 @@ __global__ void __launch_bounds__(kThreads)
     linear_db_kernel(const float *__restrict__ part, int blocks, int n, float *__restrict__ db)
 {
     grid_dep_wait();
-    grid_dep_launch();
     __shared__ float s_sum[kThreads / 32][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int col = blockIdx.x * 32 + lane;

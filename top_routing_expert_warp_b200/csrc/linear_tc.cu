@@ -11,7 +11,8 @@
 // A tile is
 //   CG = 2: 256 x 256 on a CTA pair (cta_group::2, each CTA stages 128 rows of
 //           P and 128 of Q), for large products: per SM a 64-wide k block
-//           brings 32 KB for 256 cycles of tensor work;
+//           brings 32 KB for 256 cycles of tensor work (narrower tiles, to
+//           fill the last round of pairs better, were 3 to 30 % slower);
 //   CG = 1: 128 x up to 128 on one CTA, for small ones.
 // With few rows (serving) the product is taken transposed: P is the weights
 // (128 of them are the MMA's rows) and Q the tokens (rounded up to 16 as the
@@ -63,7 +64,7 @@ struct TcParams {
     int32_t slices;
     int32_t share;           // columns of a tile that a slice's CTA finishes, even
     int32_t kblocks;
-    int32_t bn;              // columns of the MMA (CG = 1), multiple of 16
+    int32_t bn;              // columns of a tile and of the MMA: a multiple of 16 CG
     int32_t b_bytes;         // bytes of Q per CTA and stage
     int32_t act;
     int32_t swap;            // D is the output's transpose
@@ -131,32 +132,63 @@ __device__ __forceinline__ void store_run(void *base, int64_t at, bool f32, int 
     }
 }
 
-__device__ __forceinline__ void add_run(const void *base, int64_t at, bool f32, int n, float (&v)[32])
+// The same run of a row to registers (bf16: the first half of res), and its
+// addition to v.
+__device__ __forceinline__ void load_run(const void *base, int64_t at, bool f32, int n, uint4 (&res)[8])
 {
+    if (f32) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(base) + at);
 #pragma unroll
-    for (int i = 0; i < 32; i += 8) {
-        if (i >= n)
-            continue;
-        if (f32) {
-            const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + at + i);
+        for (int i = 0; i < 8; ++i)
+            res[i] = 4 * i < n ? p[i] : make_uint4(0, 0, 0, 0);
+    } else {
+        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(base) + at);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float4 w = p[h];
-                v[i + 4 * h] += w.x;
-                v[i + 4 * h + 1] += w.y;
-                v[i + 4 * h + 2] += w.z;
-                v[i + 4 * h + 3] += w.w;
-            }
-        } else {
-            const uint4 q =
-                *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(base) + at + i);
-            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        for (int i = 0; i < 4; ++i)
+            res[i] = 8 * i < n ? p[i] : make_uint4(0, 0, 0, 0);
+    }
+}
+
+__device__ __forceinline__ void add_run(const uint4 (&res)[8], bool f32, int n, float (&v)[32])
+{
+    if (f32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[4 * i] += __uint_as_float(res[i].x);
+            v[4 * i + 1] += __uint_as_float(res[i].y);
+            v[4 * i + 2] += __uint_as_float(res[i].z);
+            v[4 * i + 3] += __uint_as_float(res[i].w);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w[4] = {res[i].x, res[i].y, res[i].z, res[i].w};
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                v[i + 2 * x] += __uint_as_float(w[x] << 16);
-                v[i + 2 * x + 1] += __uint_as_float(w[x] & 0xFFFF0000u);
+                v[8 * i + 2 * x] += __uint_as_float(w[x] << 16);
+                v[8 * i + 2 * x + 1] += __uint_as_float(w[x] & 0xFFFF0000u);
             }
         }
+    }
+}
+
+// v += n bias values, the same for every lane.
+__device__ __forceinline__ void add_bias(const float *b, int n, float (&v)[32])
+{
+    if (n == 32 && reinterpret_cast<uintptr_t>(b) % 16 == 0) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            const float4 q = __ldg(reinterpret_cast<const float4 *>(b + i));
+            v[i] += q.x;
+            v[i + 1] += q.y;
+            v[i + 2] += q.z;
+            v[i + 3] += q.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < n)
+                v[i] += __ldg(b + i);
     }
 }
 
@@ -219,19 +251,19 @@ __device__ __forceinline__ void finish_block(const TcParams &p, float *st, int64
                        static_cast<int64_t>(c0) * ep.cols + r, ep.cols, n, v);
         }
     } else if (p.vec && n % 8 == 0) {
-        // every lane a piece of its own row, 16 bytes at a time
+        // every lane a piece of its own row, 16 bytes at a time; the residual's
+        // loads are on their way while the activation is computed
         if (r < p.I) {
-            if (ep.bias) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (i < n)
-                        v[i] += __ldg(ep.bias + c0 + i);
-            }
+            uint4 res[8];
+            if (ep.residual)
+                load_run(ep.residual, r * ep.ldr + c0, p.out_f32, n, res);
+            if (ep.bias)
+                add_bias(ep.bias + c0, n, v);
             if (ep.preact)
                 store_run(ep.preact, r * ep.cols + c0, false, n, v);
             act32(p.act, v);
             if (ep.residual)
-                add_run(ep.residual, r * ep.ldr + c0, p.out_f32, n, v);
+                add_run(res, p.out_f32, n, v);
             store_run(ep.out, r * ep.ldo + c0, p.out_f32, n, v);
         }
     } else {
@@ -296,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int kb_hi = SLICED ? static_cast<int>(static_cast<int64_t>(p.kblocks) * (slice + 1) / p.slices)
                              : p.kblocks;
     const int kb_half = SLICED ? (kb_lo + kb_hi + 1) / 2 : kb_hi;   // from here on in accumulator 1
-    const int tj = CG == 2 ? 256 : p.bn;     // tile columns
+    const int tj = p.bn;                     // tile columns
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -329,7 +361,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem_base = *s_tmem;
     grid_dep_wait();
-    grid_dep_launch();
 
     // consecutive tiles share their columns
     auto tile_at = [&](int u, int &i0, int &j0) {
@@ -353,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int i0, j0;
                 tile_at(u, i0, j0);
                 i0 += static_cast<int>(rank) * 128;
-                j0 += static_cast<int>(rank) * 128;
+                j0 += static_cast<int>(rank) * (tj / 2);
                 for (int kb = kb_lo; kb < kb_hi; ++kb) {
                     if (!wait(&empty[s], ph ^ 1u, s_abort)) {
                         set_status(p.status, DEV_TIMEOUT_PRODUCER);
@@ -404,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         if (lane == 0 && leader) {
             // ================= MMA issuer =================
-            const uint32_t idesc = idesc_bf16_f32(TI, CG == 2 ? 256 : p.bn) |
+            const uint32_t idesc = idesc_bf16_f32(TI, p.bn) |
                                    (P_MN ? kIdescTransA : 0u) | (Q_MN ? kIdescTransB : 0u);
             int s = 0;
             uint32_t ph = 0;
@@ -676,7 +707,7 @@ cudaError_t launch_tc(const TcParams &p, const void *P, int64_t ldp, const void 
     CUtensorMap mP, mQ;
     const bool ok = (P_MN ? make_map(&mP, P, p.I, K, ldp, BK) : make_map(&mP, P, K, p.I, ldp, 128)) &&
                     (Q_MN ? make_map(&mQ, Q, p.J, K, ldq, BK)
-                          : make_map(&mQ, Q, K, p.J, ldq, CG == 2 ? 128 : p.bn));
+                          : make_map(&mQ, Q, K, p.J, ldq, p.bn / CG));
     if (!ok)
         return cudaErrorInvalidValue;
     return p.slices > 1 ? launch_tc<CG, P_MN, Q_MN, true>(p, mP, mQ, workers, stream)
@@ -751,8 +782,8 @@ cudaError_t launch_linear_tc(const LinearGemm &L, cudaStream_t stream)
     const bool q_mn = sw ? !L.p_kmajor : !L.q_kmajor;
     const bool p_mn = sw ? !L.q_kmajor : !L.p_kmajor;
     p.bn = pl.bn;
-    p.b_bytes = pl.cg == 2 ? B_BYTES : (q_mn ? static_cast<int32_t>(ceil_div(p.bn, 64)) * 8192
-                                             : p.bn * BK * 2);
+    const int bc = p.bn / pl.cg;             // columns per CTA
+    p.b_bytes = q_mn ? static_cast<int32_t>(ceil_div(bc, 64)) * 8192 : bc * BK * 2;
     p.act = L.act;
     p.swap = sw;
     p.out_f32 = L.out_f32;

@@ -89,25 +89,6 @@ __device__ __forceinline__ uint32_t order_key(float v)
 
 constexpr uint32_t kOffKey = 0x007FFFFFu;     // of -inf
 
-// e^x in 32 bits within 4 half steps, x at most 88: 2^t with t = x log2(e)
-// rounded, then corrected by the rounding of t.  Below 2^-126 (-inf too): 0.
-__device__ __forceinline__ float exp_32(float x)
-{
-    x = fmaxf(x, -120.0f);
-    const float t = x * 1.44269504f;
-    const float lo = fmaf(x, 1.44269504f, -t);
-    float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
-    return fmaf(e * 0.693147181f, lo, e);
-}
-
-__device__ __forceinline__ float recip_32(float x)
-{
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
 __device__ __forceinline__ float key_value(uint32_t k)
 {
     return __uint_as_float((k >> 31) ? (k & 0x7FFFFFFFu) : ~k);
