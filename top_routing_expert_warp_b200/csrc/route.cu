@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, VPL == 8 ? 3 : 4)
     grid_dep_wait();
     grid_dep_launch();
     __shared__ double s_val[kWarps][32 * VPL];   // scratch of a token's choice
-    __shared__ double s_acc[kWarps][32 * VPL];   // sums of s / sum s, each lane its own
+    __shared__ double s_acc[kWarps][32 * VPL];   // sums of s / sum s, a lane's 32 apart
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int N = p.N, k = p.k;
     const int e0 = lane * VPL;
@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, VPL == 8 ? 3 : 4)
         b[i] = fmaxf(b[i], -INFINITY);
         if (!isinf(b[i]))
             bmax = fmaxf(bmax, fabsf(b[i]));
-        s_acc[warp][e0 + i] = 0.0;
+        s_acc[warp][i * 32 + lane] = 0.0;
         part[i] = 0.0f;
     }
     // Half steps of 32 bits (2^-24) that a value s + b may be off: a logistic
@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, VPL == 8 ? 3 : 4)
             held = 0;
 #pragma unroll
             for (int i = 0; i < VPL; ++i) {
-                s_acc[warp][e0 + i] += part[i];
+                s_acc[warp][i * 32 + lane] += part[i];
                 part[i] = 0.0f;
             }
         }
@@ -670,12 +670,12 @@ __global__ void __launch_bounds__(kThreads, VPL == 8 ? 3 : 4)
         // the block's sums, warp by warp in order
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
-            s_acc[warp][e0 + i] += part[i];
+            s_acc[warp][i * 32 + lane] += part[i];
         __syncthreads();
         for (int e = threadIdx.x; e < N; e += kThreads) {
             double sum = 0.0;
             for (int w = 0; w < kWarps; ++w)
-                sum += s_acc[w][e];
+                sum += s_acc[w][e % VPL * 32 + e / VPL];
             if (p.p_mean)
                 p.p_mean[e] = static_cast<float>(sum / static_cast<double>(p.T));
             else
@@ -684,28 +684,36 @@ __global__ void __launch_bounds__(kThreads, VPL == 8 ? 3 : 4)
     }
 }
 
-// p_mean from the blocks' sums: 32 experts per block, every 32nd row per warp,
-// the warps' sums added in a fixed order.
-__global__ void __launch_bounds__(1024)
-    route_mean_kernel(const double *__restrict__ p_part, int rows, int N, int64_t T,
+// p_mean from the blocks' sums (at most kRouteMaxBlocks rows): 8 experts per
+// block, every 64th row per thread with all its loads in flight, added in order;
+// then the 64 threads of an expert by a warp.
+constexpr int kMeanThreads = 512;
+__global__ void __launch_bounds__(kMeanThreads)
+    route_mean_kernel(const double *__restrict__ p_part, int rows, int N, double inv_t,
                       float *__restrict__ p_mean)
 {
     grid_dep_wait();
-    grid_dep_launch();
-    __shared__ double s_sum[32][33];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int e = blockIdx.x * 32 + lane;
-    double sum = 0.0;
-    if (e < N) {
-#pragma unroll 8
-        for (int r = warp; r < rows; r += 32)
-            sum += p_part[static_cast<int64_t>(r) * N + e];
+    __shared__ double s_sum[8][65];
+    constexpr int kLoads = (kRouteMaxBlocks + 63) / 64;
+    const int x = threadIdx.x & 7, y = threadIdx.x >> 3;
+    const int e = blockIdx.x * 8 + x;
+    double v[kLoads], sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const int r = y + 64 * i;
+        v[i] = e < N && r < rows ? p_part[static_cast<int64_t>(r) * N + e] : 0.0;
     }
-    s_sum[warp][lane] = sum;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+        sum += v[i];
+    s_sum[x][y] = sum;
     __syncthreads();
-    sum = warp_sum(s_sum[lane][warp]);          // expert `warp` of the block
-    if (lane == 0 && blockIdx.x * 32 + warp < N)
-        p_mean[blockIdx.x * 32 + warp] = static_cast<float>(sum / static_cast<double>(T));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp < 8) {
+        sum = warp_sum(s_sum[warp][lane] + s_sum[warp][lane + 32]);
+        if (lane == 0 && blockIdx.x * 8 + warp < N)
+            p_mean[blockIdx.x * 8 + warp] = static_cast<float>(sum * inv_t);
+    }
 }
 
 struct RouteGradParams {
@@ -1015,8 +1023,8 @@ cudaError_t launch_route(const RouteLaunch &L, cudaStream_t stream)
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !p.p_part)
         return e;
-    launch_k(route_mean_kernel, dim3((L.N + 31) / 32), dim3(1024), 0, stream, L.p_part, grid, L.N,
-             L.T, L.p_mean);
+    launch_k(route_mean_kernel, dim3((L.N + 7) / 8), dim3(kMeanThreads), 0, stream, L.p_part, grid,
+             L.N, 1.0 / static_cast<double>(L.T), L.p_mean);
     count_launches(1);
     return cudaGetLastError();
 }
