@@ -296,10 +296,8 @@ __device__ __forceinline__ bool choose(const RouteParams &p, const F (&v)[VPL],
     for (int i = 0; i < VPL; ++i)
         key[i] = e0 + i >= N ? K(0) : order_key(p.bias ? v[i] : static_cast<F>(l[i]));
     if (p.n_groups > 1) {
-        // (the 64-bit choice is rare: it takes the short way through scratch)
-        constexpr bool kWide = sizeof(F) == 8;
-        const int nl = kWide ? 1 : p.node_lanes, per = p.per_node;
-        const bool direct = !kWide && p.node_direct;
+        const int nl = p.node_lanes, per = p.per_node;
+        const bool direct = p.node_direct;
         const int g = lane / nl;
         const F *s_node = nullptr;
         int count = 0;
@@ -313,7 +311,7 @@ __device__ __forceinline__ bool choose(const RouteParams &p, const F (&v)[VPL],
             count = g < p.n_groups ? (per - at + nl - 1) / nl : 0;
         }
         F sum;
-        if (kWide || p.group_top > 4)
+        if (p.group_top > 4)
             sum = node_sum_any<F>(scratch + (g < p.n_groups ? g * per : 0),
                                   g < p.n_groups ? per : 0, p.group_top);
         else if (p.group_top <= 2)
@@ -421,13 +419,13 @@ __device__ __noinline__ int choose_exact(const RouteParams &p, const void *row, 
         mx = fmaxf(mx, l[i]);
     }
     mx = warp_max(mx);
-    // one expert after another through s_val: this runs for a token in hundreds
-    // or thousands, whose warp then waits for its instructions most of all
+    // through s_val, a few experts at a time: this runs for a token in hundreds or
+    // thousands, whose warp waits for its instructions as much as for its sums
     double z = 0.0;
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
         s_val[e0 + i] = l[i];
-#pragma unroll 1
+#pragma unroll 4
     for (int i = 0; i < VPL; ++i) {
         const double li = s_val[e0 + i];
         double si;
