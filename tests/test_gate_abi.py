@@ -77,7 +77,7 @@ def test_route_argument_refusals(lib):
         assert route([P(FAKE + 2) if j == i else a for j, a in enumerate(ok)]) == inv
     assert route(ws=None) == wsp and route(ws=P(FAKE + 8)) == wsp and route(nb=n - 1) == wsp
 
-    ok2 = [P(FAKE), P(FAKE), P(FAKE), None, P(FAKE)]
+    ok2 = [P(FAKE), P(FAKE), P(FAKE), None, P(FAKE + 4096)]
 
     def back(args=ok2, ws=P(FAKE), nb=n):
         return lib.moe_route_backward(c, *args, ws, nb, None)
@@ -85,6 +85,7 @@ def test_route_argument_refusals(lib):
         assert back([None if j == i else a for j, a in enumerate(ok2)]) == inv
     for i in range(5):
         assert back([P(FAKE + 2) if j == i else a for j, a in enumerate(ok2)]) == inv
+    assert back(ok2[:4] + [P(FAKE)]) == inv                   # in place
     assert back(ws=None) == wsp and back(ws=P(FAKE + 8)) == wsp and back(nb=n - 1) == wsp
 
 

@@ -378,6 +378,58 @@ def test_combine_backward_bad_rows_are_reported_and_left_out():
                              moe.workspace(cfg))
 
 
+def test_combine_backward_rows_past_32_bit_offsets():
+    T, d, k = 70000, 8192, 4
+    cfg = moe.make_config(T, d, 8, k, 8, dtype="bf16")
+    ws = torch.zeros(moe.moe_workspace_bytes(cfg), dtype=torch.uint8, device="cuda")
+    dy = torch.full((T, d), 0.5, dtype=torch.bfloat16, device="cuda")
+    yp = torch.full((T * k, d), 2.0, dtype=torch.bfloat16, device="cuda")        # 2.3e9 elements
+    inv = torch.arange(T * k - 1, -1, -1, dtype=torch.int32, device="cuda")
+    w = torch.arange(T * k, dtype=torch.float32, device="cuda").view(T, k) % 128
+    dyp, dw = torch.zeros_like(yp), torch.empty(T, k, device="cuda")
+    moe.moe_combine_backward(cfg, dy, yp, inv, w, dyp, dw, ws)
+    assert moe.moe_check_status(ws)[0] == moe.MOE_OK
+    assert torch.all(dw == d)                            # 8192 times 0.5 * 2
+    want = (w.view(-1).flip(0) * 0.5).bfloat16()
+    assert torch.equal(dyp[:, 0], want) and torch.equal(dyp[:, -1], want)
+
+
+def test_route_rows_past_32_bit_offsets():
+    T, N, k, ld = 70001, 64, 4, 20000                    # 5.6 GB from the first row to the last
+    buf = torch.empty(T * ld, device="cuda").as_strided((T, N), (ld, 1))
+    l = logits_of(T, N, 12, "f32")
+    buf.copy_(l)
+    cfg = moe.make_route_config(T, N, k, score="sigmoid", renormalize=True, ld=ld)
+    ws = moe.route_workspace(cfg)
+    idx, w = torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda")
+    moe.moe_route(cfg, buf, None, idx, w, None, ws)
+    dense = run_route(l, None, k, score="sigmoid", renorm=True, p=False)
+    assert np.array_equal(idx.cpu().numpy(), dense[0]) and np.array_equal(w.cpu().numpy(), dense[1])
+    dl = torch.empty(T * ld, device="cuda").as_strided((T, N), (ld, 1))
+    moe.moe_route_backward(cfg, buf, idx, w, None, dl, ws)
+    flat = torch.empty(T, N, device="cuda")
+    moe.moe_route_backward(moe.make_route_config(T, N, k, score="sigmoid", renormalize=True), l.cuda(),
+                           idx, w, None, flat, ws)
+    assert torch.equal(dl, flat)
+
+
+def test_route_on_a_given_stream():
+    T, N, k = 300, 64, 4
+    l = logits_of(T, N, 13, "f32")
+    want = run_route(l, None, k)
+    cfg = moe.make_route_config(T, N, k)
+    x, ws = torch.zeros(T, N, device="cuda"), moe.route_workspace(cfg)
+    idx, w = torch.zeros(T, k, dtype=torch.int32, device="cuda"), torch.zeros(T, k, device="cuda")
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(2_000_000)                     # the copy ends long after the call returns
+        x.copy_(l.cuda())
+    moe.moe_route(cfg, x, None, idx, w, None, ws, stream=s)      # in order behind the copy
+    s.synchronize()
+    assert np.array_equal(idx.cpu().numpy(), want[0]) and np.array_equal(w.cpu().numpy(), want[1])
+
+
 # ------------------------------------------------------------------ a run of them together
 class GateStep:
     """One step of a layer with a trainable gate: projection to logits, routing, dispatch, experts,

@@ -231,3 +231,28 @@ def test_linear_is_the_same_twice(shape):
         moe.moe_linear_backward(cfg, dy, x, W, None, dx, dW, db, ws)
         seen.append((y, dx, dW, db))
     assert all(torch.equal(a, b) for a, b in zip(*seen))
+
+
+@pytest.mark.parametrize("M", [70001, 40])
+def test_linear_rows_past_32_bit_offsets(M):
+    """Rows 80 kB (or 132 MB) apart: element offsets past 2^31, on tiles of tokens and transposed."""
+    K, N, ld = 64, 72, 40000 if M > 1000 else 66_000_000
+    g = torch.Generator().manual_seed(5)
+    x, W, r = ints(g, M, K).bfloat16(), ints(g, N, K).bfloat16(), ints(g, M, N).bfloat16()
+    far = lambda t: torch.empty((M - 1) * ld + t.shape[1], dtype=t.dtype,  # noqa: E731
+                                device="cuda").as_strided(t.shape, (ld, 1)).copy_(t)
+    cfg = moe.make_linear_config(M, K, N, act="relu", ldx=ld, ldy=ld, ldr=ld)
+    ws = moe.linear_workspace(cfg)
+    xd, y = far(x), far(r)
+    moe.moe_linear(cfg, xd, W.cuda(), None, y, y, None, ws)
+    z = x.double().cuda() @ W.double().cuda().t()
+    assert torch.equal(y, (z.clamp(min=0) + r.double().cuda()).bfloat16())
+    dx, dW, db = far(x), torch.empty(N, K, dtype=torch.bfloat16, device="cuda"), torch.empty(N, device="cuda")
+    flat = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+    pre = z.bfloat16()
+    moe.moe_linear_backward(cfg, y, xd, W.cuda(), pre, dx, dW, db, ws)
+    assert moe.moe_check_status(ws)[0] == moe.MOE_OK
+    dense = moe.make_linear_config(M, K, N, act="relu")
+    dW2, db2 = torch.empty_like(dW), torch.empty_like(db)
+    moe.moe_linear_backward(dense, y.contiguous(), x.cuda(), W.cuda(), pre, flat, dW2, db2, ws)
+    assert torch.equal(dx, flat) and torch.equal(dW, dW2) and torch.equal(db, db2)

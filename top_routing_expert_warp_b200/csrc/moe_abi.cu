@@ -877,7 +877,7 @@ moe_status moe_route_backward(const moe_route_config *cfg, const void *logits,
     if (!route_config_ok(cfg))
         return MOE_ERR_INVALID_ARG;
     const moe_route_config &c = *cfg;
-    if (c.T > 0 && (!logits || !dlogits || (dtopk_w && !topk_idx) ||
+    if (c.T > 0 && (!logits || !dlogits || dlogits == logits || (dtopk_w && !topk_idx) ||
                     !aligned(logits, elem_size(c.dtype)) || !aligned(dlogits, elem_size(c.dtype))))
         return MOE_ERR_INVALID_ARG;
     if (!aligned(topk_idx, 4) || !aligned(dtopk_w, 4) || !aligned(dp_mean, 4))
