@@ -362,43 +362,34 @@ __global__ void __launch_bounds__(kThreads)
     lin::put(static_cast<TO *>(ep.out) + lane * ep.ldo + n, z);
 }
 
-// V consecutive values as fp32; vec: they lie on a 16-byte boundary (or V = 1).
-template <int V>
-__device__ __forceinline__ void load_v(const float *p, float (&v)[V])
-{
-    if (V % 4 == 0) {
+// V consecutive values as they lie (on a 16-byte boundary, or V = 1), and as fp32.
+template <typename T, int V>
+struct Run {
+    static constexpr int kWords = V == 1 ? 1 : V * static_cast<int>(sizeof(T)) / 4;
+    uint32_t w[kWords];
+    __device__ __forceinline__ void load(const T *p)
+    {
+        if (V == 1) {
+            w[0] = sizeof(T) == 4 ? *reinterpret_cast<const uint32_t *>(p)
+                                  : *reinterpret_cast<const uint16_t *>(p);
+        } else {
 #pragma unroll
-        for (int i = 0; i < V / 4; ++i) {
-            const float4 w = reinterpret_cast<const float4 *>(p)[i];
-            v[4 * i] = w.x;
-            v[(4 * i + 1) % V] = w.y;
-            v[(4 * i + 2) % V] = w.z;
-            v[(4 * i + 3) % V] = w.w;
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 q = reinterpret_cast<const uint4 *>(p)[i];
+                w[(4 * i) % kWords] = q.x;
+                w[(4 * i + 1) % kWords] = q.y;
+                w[(4 * i + 2) % kWords] = q.z;
+                w[(4 * i + 3) % kWords] = q.w;
+            }
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            v[i] = p[i];
     }
-}
-
-template <int V>
-__device__ __forceinline__ void load_v(const __nv_bfloat16 *p, float (&v)[V])
-{
-    if (V == 8) {
-        const uint4 q = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[(2 * i) % V] = __uint_as_float(w[i] << 16);
-            v[(2 * i + 1) % V] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            v[i] = __bfloat162float(p[i]);
+    __device__ __forceinline__ float at(int i) const
+    {
+        if (sizeof(T) == 4)
+            return __uint_as_float(w[i % kWords]);
+        return __uint_as_float((i & 1) ? (w[i / 2 % kWords] & 0xFFFF0000u) : (w[i / 2 % kWords] << 16));
     }
-}
+};
 
 template <int V>
 __device__ __forceinline__ void store_v(float *p, const float (&v)[V])
@@ -451,22 +442,42 @@ __global__ void __launch_bounds__(kThreads)
     for (int i = 0; i < V; ++i)
         sum[i] = 0.0f;
     if (col < n) {
-#pragma unroll 4
-        for (int64_t r = r0 + warp; r < r1; r += kThreads / 32) {
-            float g[V];
-            load_v<V>(dy + r * ldy + col, g);
-            if (ACT != MOE_LINEAR_NONE) {
-                float zz[V];
-                load_v<V>(z + r * n + col, zz);
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    g[i] *= lin::act_bwd<ACT>(zz[i]);
+        // the next two rows' loads are in flight while a row is computed
+        constexpr int kAhead = 2, kStep = kThreads / 32;
+        Run<TO, V> y[kAhead];
+        Run<T, V> zz[kAhead];
+        auto fetch = [&](int slot, int64_t r) {
+            if (r < r1) {
+                y[slot].load(dy + r * ldy + col);
+                if (ACT != MOE_LINEAR_NONE)
+                    zz[slot].load(z + r * n + col);
             }
+        };
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                sum[i] += g[i];
-            if (dz)
-                store_v<V>(dz + r * ldz + col, g);
+        for (int a = 0; a < kAhead; ++a)
+            fetch(a, r0 + warp + a * kStep);
+        for (int64_t r = r0 + warp; r < r1; r += kAhead * kStep) {
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a) {
+                const int64_t row = r + a * kStep;
+                if (row >= r1)
+                    break;
+                float g[V], f[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    g[i] = y[a].at(i);
+                    f[i] = ACT != MOE_LINEAR_NONE ? zz[a].at(i) : 0.0f;
+                }
+                fetch(a, row + kAhead * kStep);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    if (ACT != MOE_LINEAR_NONE)
+                        g[i] *= lin::act_bwd<ACT>(f[i]);
+                    sum[i] += g[i];
+                }
+                if (dz)
+                    store_v<V>(dz + row * ldz + col, g);
+            }
         }
     }
     if (part) {
