@@ -10,6 +10,7 @@
 //   y  = x W^T      P = x  (k contiguous),      Q = W (k contiguous)
 //   dx = dz W       P = dz (k contiguous),      Q = W^T (j contiguous)
 //   dW = dz^T x     P = dz^T (i contiguous),    Q = x^T (j contiguous)
+#include <algorithm>
 #include <type_traits>
 
 #include "common.cuh"
@@ -583,10 +584,11 @@ SimtPlan simt_plan(int64_t I, int64_t J, int64_t K)
 {
     SimtPlan pl;
     pl.tiles = (I + TM - 1) / TM * ((J + TN - 1) / TN);
-    // about four blocks per SM, slices of at least 48 of k
-    int64_t s = 148 * 4 / pl.tiles;
-    if (s > K / 48)
-        s = K / 48;
+    // about four blocks per SM, slices of at least 96 of k, at most 16 (the last
+    // block of a tile adds them all up): 16 x 4096 x 512 took 37 us in 64 slices
+    // and 20 in 16; 64 x 1024 x 64 16 us in slices of 32, 10 of 96, 16 of 256
+    int64_t s = std::min<int64_t>(16, 148 * 4 / pl.tiles);
+    s = std::min<int64_t>(s, K / 96);
     pl.splits = static_cast<int>(s < 1 ? 1 : s);
     return pl;
 }
