@@ -148,6 +148,22 @@ def test_route_masked_and_extreme(score, nodes, bias):
         check_route(l, b, k, score=score, renorm=renorm, **kw)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("nodes", [False, True])
+@pytest.mark.parametrize("low", [-1e9, -3.0e38, -40.0])
+def test_route_bias_that_masks_or_dwarfs_the_scores(low, nodes, score):
+    """Experts held back by a large negative bias, and preferred by one far above the scores."""
+    T, N, k = 400, 64, 6
+    l = logits_of(T, N, 14, "f32")
+    b = torch.randn(N, generator=torch.Generator().manual_seed(6)) * 0.05
+    b[1::2] = low
+    b[8] = 1000.0
+    kw = dict(n_groups=8, topk_groups=3, group_top=2) if nodes else {}
+    check_route(l, b, k, score=score, renorm=True, **kw)
+    b[:] = low                                           # the scores are below the bias's last bit
+    check_route(l, b, k, score=score, renorm=True, **kw)
+
+
 def test_route_nan_counts_as_masked_and_is_reported():
     l = logits_of(9, 40, 1, "f32")
     l[3, 7] = float("nan")

@@ -425,7 +425,7 @@ __device__ __forceinline__ float bf16_bits_to_f32(uint32_t bits16)
 }
 
 // ------------------------------------------------------------------ math
-// e^x in 32 bits within 4 half steps, x at most 88: 2^t with t = x log2(e)
+// e^x in 32 bits within 6 half steps, x at most 88: 2^t with t = x log2(e)
 // rounded, then corrected by the rounding of t.  Below 2^-126 (-inf too): 0.
 __device__ __forceinline__ float exp_32(float x)
 {

@@ -206,11 +206,12 @@ __device__ __forceinline__ void list_insert(F (&a)[M], F v)
 }
 
 // Sum of the `m` (at most M) largest of the values of this lane's node, on
-// every lane of the node, largest first; -inf counts as nothing.  The lists of
-// two halves of a node merge entry by entry.
+// every lane of the node, largest first, and the sum of their absolute values;
+// -inf counts as nothing.  The lists of two halves of a node merge entry by
+// entry.
 template <int M, int VPL, typename F>
 __device__ __forceinline__ F node_sum(const F (&v)[VPL], const F *s_node, int count, int lanes,
-                                      int m)
+                                      int m, float &size)
 {
     F a[M];
 #pragma unroll
@@ -234,18 +235,22 @@ __device__ __forceinline__ F node_sum(const F (&v)[VPL], const F *s_node, int co
             list_insert<M, F>(a, b[i]);
     }
     F sum = 0;
+    size = 0.0f;
 #pragma unroll
     for (int i = 0; i < M; ++i)
-        if (i < m && a[i] != -INFINITY)
+        if (i < m && a[i] != -INFINITY) {
             sum += a[i];
+            size += fabsf(static_cast<float>(a[i]));
+        }
     return sum;
 }
 
 // Sum of the `m` largest of `per` values in shared memory, for any m: each
 // pass finds the largest one below the last taken (or one more equal to it).
 template <typename F>
-__device__ __forceinline__ F node_sum_any(const F *v, int per, int m)
+__device__ __forceinline__ F node_sum_any(const F *v, int per, int m, float &size)
 {
+    size = 0.0f;
     F sum = 0, last = INFINITY;
     int taken = 0;              // of the values equal to `last`
     for (int r = 0; r < m; ++r) {
@@ -267,6 +272,7 @@ __device__ __forceinline__ F node_sum_any(const F *v, int per, int m)
         if (best == -INFINITY)
             break;
         sum += best;
+        size += fabsf(static_cast<float>(best));
     }
     return sum;
 }
@@ -277,11 +283,21 @@ __device__ __forceinline__ double key_value_of(uint64_t k)
     return __longlong_as_double(static_cast<long long>((k >> 63) ? (k & 0x7FFFFFFFFFFFFFFFull) : ~k));
 }
 
+// Whether a >= b are far enough apart to be ordered right (or not comparable:
+// an infinity).  An expert's value is off by at most margin / 2 times 1 + |v|.
+template <typename F>
+__device__ __forceinline__ bool apart(F a, F b, F margin)
+{
+    const F size = larger(a < 0 ? -a : a, b < 0 ? -b : b);
+    return !(a - b <= margin * (F(1) + size));
+}
+
 // The choice: v = s + b of this lane's experts (-inf: switched off), K the key
 // type of F.  Lane j gets the j-th best expert in `mine` and its key in
 // `my_key`, for the `found` best: p.k of them, or with `margin` >= 0 one more,
-// and all (up to 32) that are not more than margin below the k-th.  Returns
-// whether a chosen node's score is within node_margin of the first one left out.
+// and all (up to 32) that are not apart() from the k-th.  Returns whether a
+// chosen node's score is too near the first one left out, with sums off by
+// node_margin times their size.
 template <typename F, typename K, int VPL>
 __device__ __forceinline__ bool choose(const RouteParams &p, const F (&v)[VPL],
                                        const float (&l)[VPL], F *scratch, F node_margin, F margin,
@@ -311,13 +327,14 @@ __device__ __forceinline__ bool choose(const RouteParams &p, const F (&v)[VPL],
             count = g < p.n_groups ? (per - at + nl - 1) / nl : 0;
         }
         F sum;
+        float size;
         if (p.group_top > 4)
             sum = node_sum_any<F>(scratch + (g < p.n_groups ? g * per : 0),
-                                  g < p.n_groups ? per : 0, p.group_top);
+                                  g < p.n_groups ? per : 0, p.group_top, size);
         else if (p.group_top <= 2)
-            sum = node_sum<2, VPL, F>(v, s_node, count, nl, p.group_top);
+            sum = node_sum<2, VPL, F>(v, s_node, count, nl, p.group_top, size);
         else
-            sum = node_sum<4, VPL, F>(v, s_node, count, nl, p.group_top);
+            sum = node_sum<4, VPL, F>(v, s_node, count, nl, p.group_top, size);
         K gkey = g < p.n_groups && lane == g * nl ? order_key(sum) : K(0);
         uint32_t chosen = 0;
         K m = 0;
@@ -328,7 +345,11 @@ __device__ __forceinline__ bool choose(const RouteParams &p, const F (&v)[VPL],
             if (lane == src)
                 gkey = 0;
         }
-        near = !(key_value_of(m) - key_value_of(key_max(gkey)) > node_margin);
+        if (sizeof(F) == 4) {
+            size = warp_max(g < p.n_groups ? size : 0.0f);
+            near = !(key_value_of(m) - key_value_of(key_max(gkey)) >
+                     node_margin * (static_cast<float>(p.group_top) + 2.0f * size));
+        }
         if (direct) {
             if (!((chosen >> g) & 1u)) {
 #pragma unroll
@@ -383,7 +404,7 @@ __device__ __forceinline__ bool choose(const RouteParams &p, const F (&v)[VPL],
             if (margin < 0)
                 break;
         }
-        if (found > p.k && !(key_value_of(kth) - key_value_of(m) <= margin))
+        if (found > p.k && apart(key_value_of(kth), key_value_of(m), margin))
             break;
         const bool won = lane == src;
         gone |= won ? 1u << bi : 0u;
@@ -510,24 +531,25 @@ __global__ void __launch_bounds__(kThreads, VPL == 8 ? 3 : 4)
     const bool values = p.bias != nullptr || p.n_groups > 1;   // the choice needs s + b
 
     bool bad = false;
-    float b[VPL], bmax = 0.0f;
+    float b[VPL];
     float part[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         b[i] = (p.bias && e0 + i < N) ? p.bias[e0 + i] : 0.0f;
         bad |= b[i] != b[i];
         b[i] = fmaxf(b[i], -INFINITY);
-        if (!isinf(b[i]))
-            bmax = fmaxf(bmax, fabsf(b[i]));
         s_acc[warp][i * 32 + lane] = 0.0;
         part[i] = 0.0f;
     }
-    // Half steps of 32 bits (2^-24) that a value s + b may be off: a logistic
-    // score 3.1 (4 of the exponential times 1 - s, 3 of sum and reciprocal), a
-    // softmax's share 22 (its exponential, a sum of up to 256 terms, reciprocal
-    // and product), the addition 1 + |b|.  Values further apart than twice that
-    // are ordered right.
-    const float margin = (SOFTMAX ? 0x1p-18f : 0x1p-20f) * (1.0f + warp_max(bmax));
+    // Half steps of 32 bits (2^-24) that a value v = s + b may be off: a logistic
+    // score s (6 (1 - s) + 3) <= 3.4 (6 of the exponential, 3 of sum and
+    // reciprocal), a softmax's share 22 (its exponential, a sum of up to 256
+    // terms, reciprocal and product), the addition |v|.  Two values are apart if
+    // they differ by 8 (64) half steps times 1 + |v|: more than both may be off.
+    // A sum of n such values is off by n times as much, and by half a step of
+    // each of its partial sums: n / 2 times its size at most.
+    constexpr float margin = SOFTMAX ? 0x1p-18f : 0x1p-21f;
+    const float node_margin = margin * (1.0f + 0.125f * static_cast<float>(p.group_top));
     const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
     const int64_t row_bytes = p.ld * (BF16 ? 2 : 4);
     const int64_t row_step = step * row_bytes;
@@ -615,18 +637,15 @@ __global__ void __launch_bounds__(kThreads, VPL == 8 ? 3 : 4)
 #pragma unroll
                 for (int i = 0; i < VPL; ++i)
                     s[i] = l[i] == -INFINITY ? -INFINITY : s[i] + b[i];
-                // sums of group_top values are off by that many times as much, and by
-                // half a step of every partial sum
-                const float gt = static_cast<float>(p.group_top);
                 exact = choose<float, uint32_t, VPL>(p, s, l, reinterpret_cast<float *>(s_val[warp]),
-                                                     margin * gt * (1.0f + 0.125f * gt),
-                                                     p.bias && k < N ? margin : -1.0f, found, mine, won);
+                                                     node_margin, p.bias && k < N ? margin : -1.0f,
+                                                     found, mine, won);
                 if (p.bias && !exact) {
                     // each of the found experts against the next one
                     const uint32_t nk = __shfl_down_sync(kAll, won, 1);
                     const int ne = __shfl_down_sync(kAll, mine, 1);
                     bool close = lane + 1 < found && nk > kOffKey &&
-                                 !(key_value(won) - key_value(nk) > margin);
+                                 !apart(key_value(won), key_value(nk), margin);
                     if (close)
                         // equal logits with equal biases are equal in every precision
                         close = won != nk || load_logit<BF16>(row, mine) != load_logit<BF16>(row, ne) ||
