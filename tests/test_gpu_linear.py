@@ -16,7 +16,8 @@ SHAPES = [(1, 8, 1, 0), (1, 1024, 264, 0), (2, 520, 130, 8), (7, 64, 33, 0), (16
           (17, 72, 129, 16), (63, 136, 255, 0), (64, 4096, 64, 8), (100, 264, 96, 0),
           (129, 1032, 257, 8), (256, 256, 256, 0), (300, 520, 1000, 0), (513, 192, 520, 24),
           (1030, 328, 72, 0), (1000, 2056, 1500, 0), (2100, 520, 2561, 8), (40, 4096, 4096, 0), (640, 512, 384, 0),
-          (384, 1024, 384, 0), (400, 648, 776, 8)]
+          (384, 1024, 384, 0), (400, 648, 776, 8),
+          (2100, 1400, 2561, 8), (9600, 1400, 72, 0)]
 
 
 def strided(t, pad, fill=7.0):
@@ -231,6 +232,22 @@ def test_linear_is_the_same_twice(shape):
         moe.moe_linear_backward(cfg, dy, x, W, None, dx, dW, db, ws)
         seen.append((y, dx, dW, db))
     assert all(torch.equal(a, b) for a, b in zip(*seen))
+
+
+@pytest.mark.parametrize("shape", [(40, 4096, 1000), (600, 4096, 512), (4096, 4096, 2560), (9600, 4096, 72)],
+                         ids=str)
+def test_linear_fp32_results_are_summed_in_short_chains(shape):
+    """fp32 results of bf16 operands: error of the norm at most 1.5e-6 (the tensor cores cut their
+    sums at every step, 1e-9 of the norm per k of a chain; chains are at most 1280 long)."""
+    M, K, N = shape
+    g = torch.Generator().manual_seed(2)
+    x, W = torch.randn(M, K, generator=g).bfloat16().cuda(), torch.randn(N, K, generator=g).bfloat16().cuda()
+    cfg = moe.make_linear_config(M, K, N, out_dtype="f32")
+    ws = moe.linear_workspace(cfg)
+    y = torch.empty(M, N, device="cuda")
+    moe.moe_linear(cfg, x, W, None, None, y, None, ws)
+    want = x.double() @ W.double().t()
+    assert ((y.double() - want).norm() / want.norm()).item() <= 1.5e-6
 
 
 @pytest.mark.parametrize("M", [70001, 40])

@@ -27,10 +27,15 @@
 //
 // Roles: warp 0 TMA producer, warp 1 MMA issuer, warps 2-9 epilogue (two per
 // TMEM lane quarter, on alternate 32-column steps).  Two accumulators in TMEM:
-// without slices the epilogue of a tile overlaps the products of the next; a
-// slice uses both for the halves of its k range, since the tensor cores' fp32
-// sums are cut (not rounded) at every step and their error grows with the
-// length of the chain.  Every wait is bounded.
+// the epilogue of a tile overlaps the products of the next.  Every wait is
+// bounded.
+//
+// The tensor cores' fp32 sums are cut (not rounded) at every step, an error that
+// grows with the length of the chain (1e-9 of the norm per k).  So a slice uses
+// both accumulators for the halves of its k range, and fp32 results without
+// slices are summed in chains of at most 1280, in the accumulators by turns,
+// which 16 epilogue warps add up in registers (CHAINED; 4096^3 in 124 us with
+// an error of 1e-6; 102 us in bf16 and one chain; two slices took 186 us).
 //
 // A lane of the epilogue holds a piece of a row and writes it 16 bytes at a
 // time.  Where rows are not 16-byte aligned the warp first turns its 32 x 32
@@ -57,19 +62,22 @@ constexpr int BK = 64;
 constexpr int A_BYTES = 128 * BK * 2;    // 16 KB: this CTA's 128 rows of P
 constexpr int B_BYTES = 128 * BK * 2;    // 16 KB: this CTA's up to 128 rows of Q
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr int STAGES = 6;
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr int kTurn = 33;                // floats between the columns of a turned-over block
-constexpr int TURN_BYTES = kEpiWarps * 32 * kTurn * 4;
-constexpr int AUX_BYTES = 8 * (2 * STAGES + 5) + 32;
-constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + TURN_BYTES + AUX_BYTES;
-static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of a block");
+// Epilogue warps, threads, stages and shared memory of the kernel's two forms.
+template <bool CHAINED>
+struct Form {
+    static constexpr int kEpiWarps = CHAINED ? 16 : 8;
+    static constexpr int kThreads = 64 + 32 * kEpiWarps;
+    static constexpr int kStages = CHAINED ? 5 : 6;
+    static constexpr int kTurnBytes = kEpiWarps * 32 * 32 * 4;
+    static constexpr int kSmem = 1024 + kStages * STAGE_BYTES + kTurnBytes + 8 * (2 * kStages + 5) + 32;
+    static_assert(kSmem <= 227 * 1024, "shared memory of a block");
+};
 
 struct TcParams {
     int32_t I, J;            // rows and columns of D
     int32_t i_tiles, tiles;
     int32_t slices;
+    int32_t chains;          // of sums along k, each in an accumulator of its own (CHAINED)
     int32_t share;           // columns of a tile that a slice's CTA finishes, even
     int32_t kblocks;
     int32_t bn;              // columns of a tile and of the MMA: a multiple of 16 CG
@@ -239,8 +247,13 @@ __device__ __forceinline__ void finish_run(const TcParams &p, int64_t out, int64
             store1(ep.out, out + i * out_step, p.out_f32, v[i]);
 }
 
+// AHEAD: the residual's loads are on their way while the activation is computed
+// (32 registers).
+//
 // One warp's 32 rows of D from row0 on (one per lane), nc (at most 32) columns
-// from c0 on; st: 32 x kTurn floats of this warp.
+// from c0 on; st: 32 x 32 floats of this warp, an element (column i, row r) at
+// 32 i + (r ^ i), so that neither order of access meets a bank twice.
+template <bool AHEAD>
 __device__ __forceinline__ void finish_block(const TcParams &p, float *st, int64_t row0, int c0,
                                              int nc, float (&v)[32])
 {
@@ -259,17 +272,18 @@ __device__ __forceinline__ void finish_block(const TcParams &p, float *st, int64
                        static_cast<int64_t>(c0) * ep.cols + r, ep.cols, n, v);
         }
     } else if (p.vec && n % 8 == 0) {
-        // every lane a piece of its own row, 16 bytes at a time; the residual's
-        // loads are on their way while the activation is computed
+        // every lane a piece of its own row, 16 bytes at a time
         if (r < p.I) {
             uint4 res[8];
-            if (ep.residual)
+            if (AHEAD && ep.residual)
                 load_run(ep.residual, r * ep.ldr + c0, p.out_f32, n, res);
             if (ep.bias)
                 add_bias(ep.bias + c0, n, v);
             if (ep.preact)
                 store_run(ep.preact, r * ep.cols + c0, false, n, v);
             act32(p.act, v);
+            if (!AHEAD && ep.residual)
+                load_run(ep.residual, r * ep.ldr + c0, p.out_f32, n, res);
             if (ep.residual)
                 add_run(res, p.out_f32, n, v);
             store_run(ep.out, r * ep.ldo + c0, p.out_f32, n, v);
@@ -278,11 +292,11 @@ __device__ __forceinline__ void finish_block(const TcParams &p, float *st, int64
         // turned over: the lanes hold consecutive columns, whatever their alignment
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-            st[i * kTurn + lane] = v[i];
+            st[i * 32 + (lane ^ i)] = v[i];
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-            v[i] = st[lane * kTurn + i];
+            v[i] = st[lane * 32 + (i ^ lane)];
         __syncwarp();
         if (lane < n) {
             const float b = ep.bias ? __ldg(ep.bias + c0 + lane) : 0.0f;
@@ -302,11 +316,14 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v)
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-template <int CG, bool P_MN, bool Q_MN, bool SLICED>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int CG, bool P_MN, bool Q_MN, bool SLICED, bool CHAINED>
+__global__ void __launch_bounds__(Form<CHAINED>::kThreads, 1)
     linear_tc_kernel(const __grid_constant__ CUtensorMap tmP,
                      const __grid_constant__ CUtensorMap tmQ, const TcParams p)
 {
+    static_assert(!(SLICED && CHAINED), "");
+    constexpr int STAGES = Form<CHAINED>::kStages;
+    constexpr int kEpiWarps = Form<CHAINED>::kEpiWarps;
     constexpr int TI = 128 * CG;             // tile rows
     constexpr int ACC = 128 * CG;            // TMEM columns of an accumulator
     constexpr int TMEM_COLS = 2 * ACC;
@@ -314,7 +331,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
     float *turn = reinterpret_cast<float *>(smem + STAGES * STAGE_BYTES);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * STAGE_BYTES + TURN_BYTES);
+    uint64_t *bars =
+        reinterpret_cast<uint64_t *>(smem + STAGES * STAGE_BYTES + Form<CHAINED>::kTurnBytes);
     uint64_t *full = bars;
     uint64_t *empty = bars + STAGES;
     uint64_t *acc_full = bars + 2 * STAGES;
@@ -450,54 +468,61 @@ __global__ void __launch_bounds__(kThreads, 1)
             int it = 0;
             bool ok = true;
             const uint16_t both = static_cast<uint16_t>(0x3u << lead);
-            for (int u = worker; u < p.tiles && ok; u += workers, ++it) {
-                const int a = it & 1;
-                const uint32_t aph = (it >> 1) & 1;
-                if (!wait(&acc_empty[a], aph ^ 1u, s_abort)) {
-                    set_status(p.status, DEV_TIMEOUT_MMA);
-                    *s_abort = 1;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t d_tmem = tmem_base + a * ACC;        // a = 0 in a slice
-                for (int kb = kb_lo; kb < kb_hi; ++kb) {
-                    if (!wait(&full[s], ph, s_abort)) {
+            for (int u = worker; u < p.tiles && ok; u += workers) {
+                // a tile's k range in one chain of sums, or in p.chains of them, each
+                // in the next accumulator
+                for (int ch = 0; ch < (CHAINED ? p.chains : 1) && ok; ++ch, ++it) {
+                    const int lo = CHAINED ? p.kblocks * ch / p.chains : kb_lo;
+                    const int hi = CHAINED ? p.kblocks * (ch + 1) / p.chains : kb_hi;
+                    const int a = it & 1;
+                    const uint32_t aph = (it >> 1) & 1;
+                    if (!wait(&acc_empty[a], aph ^ 1u, s_abort)) {
                         set_status(p.status, DEV_TIMEOUT_MMA);
                         *s_abort = 1;
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sa = smem_u32(smem + s * STAGE_BYTES);
-                    const uint32_t sb = sa + A_BYTES;
+                    const uint32_t d_tmem = tmem_base + a * ACC;        // a = 0 in a slice
+                    for (int kb = lo; kb < hi; ++kb) {
+                        if (!wait(&full[s], ph, s_abort)) {
+                            set_status(p.status, DEV_TIMEOUT_MMA);
+                            *s_abort = 1;
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t sa = smem_u32(smem + s * STAGE_BYTES);
+                        const uint32_t sb = sa + A_BYTES;
 #pragma unroll
-                    for (int kk = 0; kk < BK / 16; ++kk) {
-                        const uint64_t da = P_MN ? sdesc_mnmajor_sw128(sa + kk * 2048)
-                                                 : sdesc_kmajor_sw128(sa + kk * 32);
-                        const uint64_t db = Q_MN ? sdesc_mnmajor_sw128(sb + kk * 2048)
-                                                 : sdesc_kmajor_sw128(sb + kk * 32);
-                        const bool second = SLICED && kb >= kb_half;
-                        const uint32_t d = second ? d_tmem + ACC : d_tmem;
-                        const uint32_t add = (kb > (second ? kb_half : kb_lo) || kk > 0) ? 1u : 0u;
+                        for (int kk = 0; kk < BK / 16; ++kk) {
+                            const uint64_t da = P_MN ? sdesc_mnmajor_sw128(sa + kk * 2048)
+                                                     : sdesc_kmajor_sw128(sa + kk * 32);
+                            const uint64_t db = Q_MN ? sdesc_mnmajor_sw128(sb + kk * 2048)
+                                                     : sdesc_kmajor_sw128(sb + kk * 32);
+                            const bool second = SLICED && kb >= kb_half;
+                            const uint32_t d = second ? d_tmem + ACC : d_tmem;
+                            const uint32_t add = (kb > (second ? kb_half : lo) || kk > 0) ? 1u : 0u;
+                            if (CG == 2)
+                                tc_mma_bf16_pair(d, da, db, idesc, add);
+                            else
+                                tc_mma_bf16(d, da, db, idesc, add);
+                        }
                         if (CG == 2)
-                            tc_mma_bf16_pair(d, da, db, idesc, add);
+                            tc_commit_pair_mc(&empty[s], both);
                         else
-                            tc_mma_bf16(d, da, db, idesc, add);
+                            tc_commit(&empty[s]);
+                        if (++s == STAGES) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
                     }
-                    if (CG == 2)
-                        tc_commit_pair_mc(&empty[s], both);
-                    else
-                        tc_commit(&empty[s]);
-                    if (++s == STAGES) {
-                        s = 0;
-                        ph ^= 1u;
+                    if (ok) {
+                        if (CG == 2)
+                            tc_commit_pair_mc(&acc_full[a], both);
+                        else
+                            tc_commit(&acc_full[a]);
                     }
-                }
-                if (ok) {
-                    if (CG == 2)
-                        tc_commit_pair_mc(&acc_full[a], both);
-                    else
-                        tc_commit(&acc_full[a]);
                 }
             }
         }
@@ -505,47 +530,94 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ================= epilogue (this CTA's 128 rows) =================
         const int q = warp & 3;                  // TMEM lanes of this warp
         const int half = (warp - 2) >> 2;
-        float *st = turn + (warp - 2) * 32 * kTurn;
+        float *st = turn + (warp - 2) * 32 * 32;
         const uint32_t lead_empty[2] = {
             CG == 2 ? mapa_shared(smem_u32(&acc_empty[0]), lead) : 0u,
             CG == 2 ? mapa_shared(smem_u32(&acc_empty[1]), lead) : 0u};
         int it = 0;
-        for (int u = worker; u < p.tiles; u += workers, ++it) {
-            int i0, j0;
-            tile_at(u, i0, j0);
-            const int a = it & 1;
-            const uint32_t aph = (it >> 1) & 1;
+        auto acc_wait = [&](int a, uint32_t aph) {
             const bool got = wait(&acc_full[a], aph, s_abort);
-            if (!__all_sync(0xffffffffu, got)) {
-                if (lane == 0) {
-                    set_status(p.status, DEV_TIMEOUT_EPILOGUE);
-                    *s_abort = 1;
-                }
-                break;
+            if (__all_sync(0xffffffffu, got)) {
+                tc_fence_after();
+                return true;
             }
-            if (SLICED)
-                break;                           // one tile; the slices meet below
-            tc_fence_after();
-            const uint32_t tacc = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + a * ACC;
-            const int64_t row0 = static_cast<int64_t>(i0) + rank * 128 + q * 32;
-#pragma unroll 1
-            for (int c = half * 32; c < tj; c += 64) {
-                if (row0 >= p.I || j0 + c >= p.J)
-                    break;
-                uint32_t v[32];
-                float o[32];
-                tmem_ld32(tacc + c, v);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    o[i] = __uint_as_float(v[i]);
-                finish_block(p, st, row0, j0 + c, 32, o);
+            if (lane == 0) {
+                set_status(p.status, DEV_TIMEOUT_EPILOGUE);
+                *s_abort = 1;
             }
+            return false;
+        };
+        auto acc_release = [&](int a) {
             tc_fence_before();
             if (CG == 2 && !leader)
                 mbar_arrive_cluster(lead_empty[a]);
             else
                 mbar_arrive(&acc_empty[a]);
+        };
+        const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
+        if (SLICED) {
+            acc_wait(0, 0);                      // one tile; the slices meet below
+        } else if (CHAINED) {
+            // four warps per row quarter, up to 64 columns each: the chains' sums
+            // are added up in registers
+            constexpr int CW = CG * 32;
+            for (int u = worker; u < p.tiles; u += workers) {
+                int i0, j0;
+                tile_at(u, i0, j0);
+                const int64_t row0 = static_cast<int64_t>(i0) + rank * 128 + q * 32;
+                float o[CW / 32][32];
+                bool ok = true;
+                for (int ch = 0; ch < p.chains && ok; ++ch, ++it) {
+                    const int a = it & 1;
+                    ok = acc_wait(a, (it >> 1) & 1);
+                    if (!ok)
+                        break;
+#pragma unroll
+                    for (int h = 0; h < CW / 16; ++h) {
+                        const int c = half * CW + h * 16;
+                        uint32_t v[16];
+                        tmem_ld16(tmem_base + lanes + a * ACC + (c < tj ? c : 0), v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float &sum = o[h / 2][h % 2 * 16 + i];
+                            sum = ch == 0 ? __uint_as_float(v[i]) : sum + __uint_as_float(v[i]);
+                        }
+                    }
+                    acc_release(a);
+                }
+                if (!ok)
+                    break;
+#pragma unroll
+                for (int h = 0; h < CW / 32; ++h) {
+                    const int c = half * CW + h * 32;
+                    if (c < tj && row0 < p.I && j0 + c < p.J)
+                        finish_block<false>(p, st, row0, j0 + c, 32, o[h]);
+                }
+            }
+        } else {
+            for (int u = worker; u < p.tiles; u += workers, ++it) {
+                int i0, j0;
+                tile_at(u, i0, j0);
+                const int a = it & 1;
+                if (!acc_wait(a, (it >> 1) & 1))
+                    break;
+                const int64_t row0 = static_cast<int64_t>(i0) + rank * 128 + q * 32;
+#pragma unroll 1
+                for (int c = half * 32; c < tj; c += 64) {
+                    if (row0 >= p.I || j0 + c >= p.J)
+                        break;
+                    uint32_t v[32];
+                    float o[32];
+                    tmem_ld32(tmem_base + lanes + a * ACC + c, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        o[i] = __uint_as_float(v[i]);
+                    finish_block<true>(p, st, row0, j0 + c, 32, o);
+                }
+                acc_release(a);
+            }
         }
     }
 
@@ -596,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp >= 2) {
             // this CTA's columns, half of them per warp of a row quarter
             const float *sum = reinterpret_cast<const float *>(smem);
-            float *st = turn + (warp - 2) * 32 * kTurn;
+            float *st = turn + (warp - 2) * 32 * 32;
             const int wh = w / 2 < 32 ? w / 2 : 32;
             const int64_t row0 = static_cast<int64_t>(i0) + rank * 128 + q * 32;
             for (int c = half * wh; c < w; c += 2 * wh) {
@@ -616,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (i < nc)
                             o[i] += sum[(s * w + c + i) * 128 + r_local];
                 }
-                finish_block(p, st, row0, j0 + col, nc, o);
+                finish_block<true>(p, st, row0, j0 + col, nc, o);
             }
         }
     }
@@ -677,14 +749,15 @@ bool make_map(CUtensorMap *m, const void *base, int64_t inner, int64_t outer, in
            CUDA_SUCCESS;
 }
 
-template <int CG, bool P_MN, bool Q_MN, bool SLICED>
+template <int CG, bool P_MN, bool Q_MN, bool SLICED, bool CHAINED>
 cudaError_t launch_tc(const TcParams &p, const CUtensorMap &mP, const CUtensorMap &mQ, int workers,
                       cudaStream_t stream)
 {
     static DeviceOnce once;
     cudaError_t e = device_once(once, nullptr, [](int *) {
-        return cudaFuncSetAttribute(linear_tc_kernel<CG, P_MN, Q_MN, SLICED>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+        return cudaFuncSetAttribute(linear_tc_kernel<CG, P_MN, Q_MN, SLICED, CHAINED>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    Form<CHAINED>::kSmem);
     });
     if (e != cudaSuccess)
         return e;
@@ -698,12 +771,12 @@ cudaError_t launch_tc(const TcParams &p, const CUtensorMap &mP, const CUtensorMa
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.gridDim = dim3(cluster * static_cast<unsigned>(workers), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.blockDim = dim3(Form<CHAINED>::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = Form<CHAINED>::kSmem;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, linear_tc_kernel<CG, P_MN, Q_MN, SLICED>, mP, mQ, p);
+    e = cudaLaunchKernelEx(&cfg, linear_tc_kernel<CG, P_MN, Q_MN, SLICED, CHAINED>, mP, mQ, p);
     count_launches(1);
     return e;
 }
@@ -718,8 +791,12 @@ cudaError_t launch_tc(const TcParams &p, const void *P, int64_t ldp, const void 
                           : make_map(&mQ, Q, K, p.J, ldq, p.bn / CG));
     if (!ok)
         return cudaErrorInvalidValue;
-    return p.slices > 1 ? launch_tc<CG, P_MN, Q_MN, true>(p, mP, mQ, workers, stream)
-                        : launch_tc<CG, P_MN, Q_MN, false>(p, mP, mQ, workers, stream);
+    if (p.slices > 1)
+        return launch_tc<CG, P_MN, Q_MN, true, false>(p, mP, mQ, workers, stream);
+    if constexpr (!P_MN && !Q_MN)            // fp32 results: forward products only
+        if (p.chains > 1)
+            return launch_tc<CG, P_MN, Q_MN, false, true>(p, mP, mQ, workers, stream);
+    return launch_tc<CG, P_MN, Q_MN, false, false>(p, mP, mQ, workers, stream);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -730,6 +807,7 @@ struct Plan {
     bool swap;               // the transposed product
     int bn;                  // tile columns
     int slices;              // of k per tile
+    int chains;              // of sums along k per tile
     int64_t tiles;
 };
 
@@ -759,10 +837,8 @@ Plan plan_of(int64_t I, int64_t J, int64_t K, bool may_swap, bool out_f32)
     for (int n = 2; n <= most; ++n)
         if (pl.tiles <= kHeld[n * pl.cg] && kb >= n * 2)
             pl.slices = n;
-    // fp32 results: chains of at most 1280 of k per accumulator (of two), as far as slices go
-    if (out_f32 && K > 1024)
-        while (pl.slices < most && (pl.slices == 1 || K > 2560 * pl.slices))
-            ++pl.slices;
+    // fp32 results without slices: chains of at most 1280 of k
+    pl.chains = out_f32 && pl.slices == 1 ? static_cast<int>(ceil_div(kb, 20)) : 1;
     return pl;
 }
 
@@ -783,6 +859,7 @@ cudaError_t launch_linear_tc(const LinearGemm &L, cudaStream_t stream)
         return cudaErrorInvalidValue;
     p.tiles = static_cast<int32_t>(pl.tiles);
     p.slices = pl.slices;
+    p.chains = pl.chains;
     // shares in whole 16-byte pieces of a row, twice (two warps); transposed: of any size
     const int unit = sw ? 2 : 16;
     p.share = static_cast<int32_t>(ceil_div(ceil_div(pl.bn, pl.slices), unit) * unit);
