@@ -344,7 +344,8 @@ size_t moe_route_workspace_bytes(const moe_route_config *cfg);
  * A logit of -inf (or a bias of -inf) switches the expert off for the token:
  * it ranks behind every other, lowest index first, -inf logits score 0, and a
  * node's score leaves it out; a token without any expert left gets the lowest
- * indices with weight 0 (for a -inf logit) and adds nothing to p_mean.  +inf
+ * indices with weight 0 (for a -inf logit) and adds nothing to p_mean (it
+ * still takes rows in moe_dispatch).  +inf
  * counts as the largest finite fp32 value.  A NaN logit or bias counts as
  * -inf and sets a bit of the status word.
  * Rows of topk_idx and topk_w beyond T are not written; T = 0 zeroes p_mean. */

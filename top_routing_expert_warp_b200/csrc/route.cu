@@ -793,6 +793,15 @@ __device__ __forceinline__ void logistic(float l, float &s, float &om)
     om = l > 0.0f ? tr : r;
 }
 
+// The same for every expert of a row: below -88 both come out 0, as does what
+// they are multiplied into.
+__device__ __forceinline__ void logistic_pair(float l, float &s, float &om)
+{
+    const float t = exp_32(fminf(-l, 88.0f));
+    s = recip_32(1.0f + t);
+    om = t * s;
+}
+
 // With c = dp_mean / T, q = s / sum s, g = scale * dtopk_w, and over the
 // chosen slots r = s / sum s (renormalised):
 //   sigmoid: dl_e = (1 - s_e) * (q_e (c_e - sum c q) + [e chosen] u_e),
@@ -890,7 +899,7 @@ __global__ void __launch_bounds__(kThreads, 4)
         } else {
 #pragma unroll
             for (int i = 0; i < VPL; ++i)
-                logistic(l[i], s[i], om[i]);
+                logistic_pair(l[i], s[i], om[i]);
         }
         float rz = 0.0f;
         if (SOFTMAX || p.dp_mean) {
