@@ -64,7 +64,7 @@ struct TileLoad {
             const bool inside = own < owns && k < k1;
             const int64_t left = K_CONTIG ? k1 - k : owns - own;
             if (inside && left >= 4) {
-                const float4 q = *reinterpret_cast<const float4 *>(at);
+                const float4 q = __ldcg(reinterpret_cast<const float4 *>(at));
                 v[h][0] = q.x;
                 v[h][1] = q.y;
                 v[h][2] = q.z;
@@ -72,7 +72,7 @@ struct TileLoad {
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    v[h][i] = inside && i < left ? at[i] : 0.0f;
+                    v[h][i] = inside && i < left ? __ldcg(at + i) : 0.0f;
             }
         }
     }
@@ -100,6 +100,7 @@ struct SimtParams {
     int64_t I, K;
     int32_t J, i_tiles, splits, act;
     int32_t vec;             // output rows start on 16-byte boundaries
+    int32_t first_of_two, second_of_two;     // see LinearGemm
     lin::Epilogue ep;
     float *part;             // [units][64][64]
     uint32_t *tickets;       // [tiles], zero between launches
@@ -137,9 +138,8 @@ __device__ __forceinline__ void act_all(float (&v)[8][4])
 // library product reaches.  8 x 8 outputs per thread read half as much but
 // left too few warps: 61 and 430 us.
 template <bool P_K, bool Q_K>
-__global__ void __launch_bounds__(kGemmThreads) linear_simt_kernel(const __grid_constant__ SimtParams p)
+__device__ __forceinline__ void simt_tile(const SimtParams &p)
 {
-    grid_dep_wait();
     __shared__ __align__(16) float s_p[2][TK][TM + kPad];
     __shared__ __align__(16) float s_q[2][TK][TN + kPad];
     __shared__ uint32_t s_last;
@@ -282,6 +282,18 @@ __global__ void __launch_bounds__(kGemmThreads) linear_simt_kernel(const __grid_
                 if (x < rows && y < n)
                     o[x * ep.ldo + y] = out[x][y];
     }
+}
+
+template <bool P_K, bool Q_K>
+__global__ void __launch_bounds__(kGemmThreads) linear_simt_kernel(const __grid_constant__ SimtParams p)
+{
+    if (!p.second_of_two)
+        grid_dep_wait();
+    if (p.first_of_two)
+        grid_dep_launch();
+    simt_tile<P_K, Q_K>(p);
+    if (p.second_of_two)
+        grid_dep_wait();
 }
 
 // Few rows (serving): y[m, n] = act(sum_k x[m, k] W[n, k] + bias) + residual.
@@ -624,6 +636,8 @@ cudaError_t launch_linear_simt(const LinearGemm &L, cudaStream_t stream)
     p.ep = epilogue_of(L);
     p.part = L.part;
     p.tickets = L.tickets;
+    p.first_of_two = L.first_of_two;
+    p.second_of_two = L.second_of_two;
     auto kernel = L.p_kmajor ? (L.q_kmajor ? linear_simt_kernel<true, true>
                                            : linear_simt_kernel<true, false>)
                              : linear_simt_kernel<false, false>;

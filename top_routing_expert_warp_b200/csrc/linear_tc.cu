@@ -86,6 +86,7 @@ struct TcParams {
     int32_t swap;            // D is the output's transpose
     int32_t out_f32;
     int32_t vec;             // rows of every output start on 16-byte boundaries
+    int32_t first_of_two, second_of_two;     // see LinearGemm
     lin::Epilogue ep;        // in terms of the output
     uint32_t *status;
 };
@@ -386,7 +387,10 @@ __global__ void __launch_bounds__(Form<CHAINED>::kThreads, 1)
         cluster_sync_all();      // the peer's barriers exist before any remote arrive
     tc_fence_after();
     const uint32_t tmem_base = *s_tmem;
-    grid_dep_wait();
+    if (!p.second_of_two)
+        grid_dep_wait();
+    if (p.first_of_two)
+        grid_dep_launch();
 
     // consecutive tiles share their columns
     auto tile_at = [&](int u, int &i0, int &j0) {
@@ -716,6 +720,8 @@ __global__ void __launch_bounds__(Form<CHAINED>::kThreads, 1)
         else
             tmem_dealloc(tmem_base, TMEM_COLS);
     }
+    if (p.second_of_two)
+        grid_dep_wait();
 }
 
 typedef CUresult (*PFN_encode)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -887,6 +893,8 @@ cudaError_t launch_linear_tc(const LinearGemm &L, cudaStream_t stream)
     p.ep.rows = static_cast<int32_t>(L.I);
     p.ep.cols = L.J;
     p.status = L.status;
+    p.first_of_two = L.first_of_two;
+    p.second_of_two = L.second_of_two;
     const void *P = sw ? L.Q : L.P, *Q = sw ? L.P : L.Q;
     const int64_t ldp = sw ? L.ldq : L.ldp, ldq = sw ? L.ldp : L.ldq;
     // a cluster of slices takes one tile; without slices the CTAs (pairs) stay

@@ -470,7 +470,7 @@ bool linear_config_ok(const moe_linear_config *c)
 }
 
 struct LinearLayout {
-    size_t status, tickets, part, db_part, dz, total;
+    size_t status, tickets, part, tickets2, part2, db_part, dz, total;
     int64_t ldz;
 };
 
@@ -492,11 +492,14 @@ LinearLayout linear_layout(const moe_linear_config &c, bool backward)
             return moe::simt_plan_part_bytes(moe::simt_plan(I, J, K));
         };
         size_t most = part(c.M, c.n_out, c.n_in);
-        if (backward) {
+        if (backward)
             most = std::max(most, part(c.M, c.n_in, c.n_out));
-            most = std::max(most, part(c.n_out, c.n_in, c.M));
-        }
         L.part = take(most);
+        if (backward) {
+            // dW runs beside dx, with scratch of its own
+            L.tickets2 = take(moe::kLinearMaxTickets * sizeof(uint32_t));
+            L.part2 = take(part(c.n_out, c.n_in, c.M));
+        }
     }
     if (backward) {
         L.db_part = take(static_cast<size_t>(moe::kDzMaxRowBlocks) * c.n_out * sizeof(float));
@@ -1042,6 +1045,7 @@ moe_status moe_linear_backward(const moe_linear_config *cfg, const void *dy, con
         G.K = c.n_out;
         G.out = dx;
         G.ldo = c.ldx;
+        G.first_of_two = dW != nullptr;
         MOE_CUDA(launch_linear(G, s));
     }
     if (dW) {
@@ -1052,6 +1056,10 @@ moe_status moe_linear_backward(const moe_linear_config *cfg, const void *dy, con
         G.K = c.M;
         G.out = dW;
         G.ldo = c.n_in;
+        G.tickets = reinterpret_cast<uint32_t *>(ws + L.tickets2);
+        G.part = reinterpret_cast<float *>(ws + L.part2);
+        G.first_of_two = false;
+        G.second_of_two = dx != nullptr;
         MOE_CUDA(launch_linear(G, s));
     }
     return MOE_OK;
