@@ -285,11 +285,12 @@ struct LinearGemm {
     float *part;             // partial tiles, simt_plan_part_bytes (fp32 operands)
     uint32_t *tickets;       // kLinearMaxTickets words, zero between launches (fp32 operands)
     uint32_t *status;
-    // Two products in a row that need the same earlier kernels and not one
+    // Two launches in a row that need the same earlier kernels and not one
     // another run side by side: the first lets the next launch start once its own
     // wait is over (so all that came before is complete), the second starts
     // without a wait and waits for the first before it ends, so that what comes
-    // after it finds both complete.  They share no scratch.
+    // after it finds both complete.  They share no scratch.  (In a row of three
+    // the middle one is both.)
     bool first_of_two, second_of_two;
 };
 // bf16 operands on the tensor cores: see linear_tc.cu.

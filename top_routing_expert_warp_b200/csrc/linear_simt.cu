@@ -521,6 +521,7 @@ __global__ void __launch_bounds__(kThreads)
     linear_db_kernel(const float *__restrict__ part, int blocks, int n, float *__restrict__ db)
 {
     grid_dep_wait();
+    grid_dep_launch();      // the products need dz, not this
     __shared__ float s_sum[kThreads / 32][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int col = blockIdx.x * 32 + lane;

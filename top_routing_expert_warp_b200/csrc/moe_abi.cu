@@ -1046,6 +1046,7 @@ moe_status moe_linear_backward(const moe_linear_config *cfg, const void *dy, con
         G.out = dx;
         G.ldo = c.ldx;
         G.first_of_two = dW != nullptr;
+        G.second_of_two = db != nullptr;       // beside the column sums' last kernel
         MOE_CUDA(launch_linear(G, s));
     }
     if (dW) {
@@ -1059,7 +1060,7 @@ moe_status moe_linear_backward(const moe_linear_config *cfg, const void *dy, con
         G.tickets = reinterpret_cast<uint32_t *>(ws + L.tickets2);
         G.part = reinterpret_cast<float *>(ws + L.part2);
         G.first_of_two = false;
-        G.second_of_two = dx != nullptr;
+        G.second_of_two = dx != nullptr || db != nullptr;
         MOE_CUDA(launch_linear(G, s));
     }
     return MOE_OK;
