@@ -812,8 +812,8 @@ __device__ __forceinline__ void logistic_pair(float l, float &s, float &om)
 // not underflow.  One warp per token: the logits are read once and the
 // gradient is written once (2 T N values, the bound by bytes), the k chosen
 // experts' gradients a second time by the lanes that hold the slots.  65536 x
-// 256 fp32 in 36 us, 58 % of a plain copy's rate; bound by issue (0.7 per cycle,
-// 424 instructions per token).
+// 256 fp32 in 36 us, 60 % of a plain copy's rate; bound by issue (0.7 per cycle,
+// some 400 instructions per token).
 template <int VPL, bool BF16, bool SOFTMAX>
 __global__ void __launch_bounds__(kThreads, 4)
     route_grad_kernel(const __grid_constant__ RouteGradParams p)
