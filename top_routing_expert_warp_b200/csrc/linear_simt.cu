@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kGemmThreads) linear_simt_kernel(const __grid_
 // WPR warps per output n read its weights once, 16 bytes per lane with 8 loads
 // in flight, next to the same places of the rows of x (in L1); the warps' sums
 // are added in order.  Bound by the weights' bytes and the launch: one row of
-// 7168 -> 2048 bf16 in 8.8 us from HBM, 3.3 TB/s with the launch in it.
+// 7168 -> 2048 bf16 in 8.1 us from HBM, 3.6 TB/s with the launch in it.
 template <typename T, typename TO, int MR>
 __global__ void __launch_bounds__(kThreads)
     linear_rows_kernel(const T *__restrict__ x, int64_t ldx, const T *__restrict__ W, int M, int K,
@@ -559,9 +559,12 @@ lin::Epilogue epilogue_of(const LinearGemm &L)
 template <typename T, typename TO>
 void run_rows(const LinearGemm &L, cudaStream_t stream)
 {
-    // warps per output so that at least 40 warps run on each SM
+    // warps per output so that at least 24 warps run on each SM, 40 where more
+    // rows make each wait longer (4096 -> 4096: one bf16 row 8.3 us with 24, 9.5
+    // with 40; four fp32 rows 36 and 26)
+    const int64_t warps = L.I <= 2 ? 148 * 24 : 148 * 40;
     int wpr = 1;
-    while (wpr < 8 && static_cast<int64_t>(L.J) * wpr < 148 * 40)
+    while (wpr < 8 && static_cast<int64_t>(L.J) * wpr < warps)
         wpr *= 2;
     const int per = kThreads / 32 / wpr;
     auto kernel = L.I == 1 ? linear_rows_kernel<T, TO, 1>
