@@ -44,9 +44,13 @@
  *        Ws1, Ws3 [Hs, d], Ws2 [d, Hs]  the always-on shared expert
  *   - The workspace is one device buffer of at least moe_workspace_bytes(cfg)
  *     bytes, 256-byte aligned, zero-filled by the caller once before its first
- *     use (the status word must start at zero).  One workspace serves every
- *     entry point for that configuration.  Calls that share a workspace must
- *     be ordered on one stream.
+ *     use.  What has to be zero are its first MOE_WORKSPACE_HEAD bytes (the
+ *     status word and counters, which every call leaves at zero but for a
+ *     recorded problem); all behind them is written before it is read.  So one
+ *     buffer that is large enough serves every entry point and every
+ *     configuration, in turn, the workspaces of moe_route and moe_linear
+ *     included; after anything else wrote to it, its head is zeroed again.
+ *     Calls that share a workspace must be ordered on one stream.
  */
 #ifndef MOE_B200_H
 #define MOE_B200_H
@@ -69,6 +73,9 @@ typedef enum moe_status {
 } moe_status;
 
 enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2 };
+
+/* Bytes at the start of every workspace that must be zero before its first use. */
+enum { MOE_WORKSPACE_HEAD = 4352 };
 
 /* Gate modes.
  *  MOE_GATE_TOPK_THEN_SOFTMAX ("mode R"): softmax over the k selected logits

@@ -27,6 +27,7 @@ MOE_GATE_TOPK_THEN_SOFTMAX, MOE_GATE_SOFTMAX_THEN_TOPK = 0, 1
 MOE_ACT_RELU, MOE_ACT_SWIGLU = 0, 1
 MOE_OVERFLOW_DROP, MOE_OVERFLOW_FALLBACK = 0, 1
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_WORKSPACE_HEAD = 4352      # bytes at a workspace's start that must be zero before its first use
 (MOE_LINEAR_NONE, MOE_LINEAR_RELU, MOE_LINEAR_SILU, MOE_LINEAR_GELU,
  MOE_LINEAR_GELU_TANH) = range(5)
 

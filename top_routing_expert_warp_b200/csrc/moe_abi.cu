@@ -61,6 +61,17 @@ int elem_size(int dt) { return dt == MOE_F32 ? 4 : (dt == MOE_BF16 ? 2 : 1); }
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Every workspace starts with the same head: the status word's 256 bytes (with
+// the ticket of the single-launch layer behind it), then the tickets of sliced
+// fp32 products, for two launches side by side.  They are all that has to be
+// zero between calls, so a buffer may serve any configuration, whatever another
+// one left behind the head.
+constexpr size_t kHeadTickets = 256;
+constexpr size_t kHeadTickets2 = kHeadTickets + moe::kLinearMaxTickets * sizeof(uint32_t);
+static_assert(kHeadTickets2 + moe::kLinearMaxTickets * sizeof(uint32_t) == MOE_WORKSPACE_HEAD &&
+                  MOE_WORKSPACE_HEAD % 256 == 0,
+              "the head that the header promises");
+
 // Offsets of the workspace regions (bytes from the workspace start).
 struct Layout {
     size_t status, p_part, logits, topk_idx, topk_w, p_mean, counts, offsets, block_base, perm,
@@ -139,7 +150,7 @@ Layout layout_of(const moe_config &c)
         o += up256(bytes);
         return at;
     };
-    L.status = take(256);
+    L.status = take(MOE_WORKSPACE_HEAD);
     L.p_part = take(static_cast<size_t>(moe::kRouterMaxBlocks) * N * sizeof(double));
     L.logits = take(c.dtype == MOE_BF16
                         ? static_cast<size_t>(moe::router_ksplit_cap(c.T, c.N)) * T * N * 4 : 0);
@@ -433,8 +444,8 @@ bool route_config_ok(const moe_route_config *c)
     return true;
 }
 
-// Status word, then the blocks' sums of the scores.
-constexpr size_t kRoutePart = 256;
+// The head, then the blocks' sums of the scores.
+constexpr size_t kRoutePart = MOE_WORKSPACE_HEAD;
 size_t route_workspace(const moe_route_config &c)
 {
     return kRoutePart + up256(static_cast<size_t>(moe::kRouteMaxBlocks) * c.N * sizeof(double));
@@ -470,7 +481,7 @@ bool linear_config_ok(const moe_linear_config *c)
 }
 
 struct LinearLayout {
-    size_t status, tickets, part, tickets2, part2, db_part, dz, total;
+    size_t head, part, part2, db_part, dz, total;
     int64_t ldz;
 };
 
@@ -485,9 +496,8 @@ LinearLayout linear_layout(const moe_linear_config &c, bool backward)
     };
     const int64_t es = elem_size(c.dtype);
     L.ldz = (c.n_out + 7) / 8 * 8;
-    L.status = take(256);
+    L.head = take(MOE_WORKSPACE_HEAD);
     if (c.dtype == MOE_F32 && c.M > 0) {
-        L.tickets = take(moe::kLinearMaxTickets * sizeof(uint32_t));
         auto part = [&](int64_t I, int64_t J, int64_t K) {
             return moe::simt_plan_part_bytes(moe::simt_plan(I, J, K));
         };
@@ -495,11 +505,8 @@ LinearLayout linear_layout(const moe_linear_config &c, bool backward)
         if (backward)
             most = std::max(most, part(c.M, c.n_in, c.n_out));
         L.part = take(most);
-        if (backward) {
-            // dW runs beside dx, with scratch of its own
-            L.tickets2 = take(moe::kLinearMaxTickets * sizeof(uint32_t));
+        if (backward)            // dW runs beside dx, with scratch of its own
             L.part2 = take(part(c.n_out, c.n_in, c.M));
-        }
     }
     if (backward) {
         L.db_part = take(static_cast<size_t>(moe::kDzMaxRowBlocks) * c.n_out * sizeof(float));
@@ -511,8 +518,8 @@ LinearLayout linear_layout(const moe_linear_config &c, bool backward)
 
 void linear_scratch(moe::LinearGemm *G, uint8_t *ws, const LinearLayout &L)
 {
-    G->status = reinterpret_cast<uint32_t *>(ws + L.status);
-    G->tickets = reinterpret_cast<uint32_t *>(ws + L.tickets);
+    G->status = reinterpret_cast<uint32_t *>(ws + L.head);
+    G->tickets = reinterpret_cast<uint32_t *>(ws + kHeadTickets);
     G->part = reinterpret_cast<float *>(ws + L.part);
 }
 
@@ -1057,7 +1064,7 @@ moe_status moe_linear_backward(const moe_linear_config *cfg, const void *dy, con
         G.K = c.M;
         G.out = dW;
         G.ldo = c.n_in;
-        G.tickets = reinterpret_cast<uint32_t *>(ws + L.tickets2);
+        G.tickets = reinterpret_cast<uint32_t *>(ws + kHeadTickets2);
         G.part = reinterpret_cast<float *>(ws + L.part2);
         G.first_of_two = false;
         G.second_of_two = dx != nullptr || db != nullptr;
