@@ -1,0 +1,61 @@
+"""Routing at the limits of its scores and masks, on the GPU against plain definitions in 64 bits
+(gate_ref)."""
+import numpy as np
+import pytest
+import torch
+
+import gate_ref
+import top_routing_expert_warp_b200 as moe
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+
+
+def run(l, bias, k, **kw):
+    T, N = l.shape
+    cfg = moe.make_route_config(T, N, k, dtype="f32" if l.dtype is torch.float32 else "bf16",
+                                renormalize=kw.pop("renorm", False), **kw)
+    ws = moe.route_workspace(cfg)
+    idx = torch.full((T, k), -9, dtype=torch.int32, device="cuda")
+    w, p = torch.full((T, k), -9.0, device="cuda"), torch.full((N,), -9.0, device="cuda")
+    moe.moe_route(cfg, l.cuda(), None if bias is None else bias.cuda(), idx, w, p, ws)
+    assert moe.moe_check_status(ws)[0] == moe.MOE_OK
+    return idx.cpu().numpy(), w.cpu().numpy(), p.cpu().numpy()
+
+
+def check(l, bias, k, **kw):
+    idx, w, p = run(l, bias, k, **kw)
+    ri, rw, rp = gate_ref.route(l.float().numpy(), None if bias is None else bias.numpy(), k, **kw)
+    assert np.array_equal(idx, ri)
+    # at most 16 fp32 operations of half a step each, on positive terms
+    np.testing.assert_allclose(w, rw, rtol=2.0 ** -20, atol=1e-37)
+    np.testing.assert_allclose(p, rp, rtol=2.0 ** -20, atol=1e-37)
+    return p
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("N", [40, 128, 256])
+@pytest.mark.parametrize("top", [2.0, -30.0, -59.0, -61.0])
+def test_an_expert_off_in_every_row_has_no_share(top, N, score):
+    g = torch.Generator().manual_seed(N)
+    l = torch.rand(37, N, generator=g) * 4 + (top - 4)
+    l[:, 7] = -INF
+    l[:, N - 1] = -INF
+    for bias in (None, torch.randn(N, generator=g) * 0.05):
+        p = check(l, bias, 3, score=score)
+        assert p[7] == 0 and p[N - 1] == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("N", [40, 256])
+def test_logistic_scores_far_below_the_rows_largest(N, dtype):
+    """One row each, so that p is that row's shares: the largest logit is -59 and the others lie
+    where e^l is near the smallest fp32 values, or are off."""
+    g = torch.Generator().manual_seed(3)
+    for low in (-70.0, -79.5, -81.0, -84.0, -86.0, -INF):
+        l = torch.rand(1, N, generator=g) + low
+        l[0, 9] = -59.0
+        p = check(l.to(dtype), None, 3, score="sigmoid")
+        if low == -INF:
+            assert p[9] == 1.0 and np.count_nonzero(p) == 1

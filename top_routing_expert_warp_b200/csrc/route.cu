@@ -596,7 +596,8 @@ __global__ void __launch_bounds__(kThreads, VPL == 8 ? 3 : 4)
             } else {
 #pragma unroll
                 for (int i = 0; i < VPL; ++i) {
-                    s[i] = recip_32(1.0f + exp_32(fminf(-l[i], 80.0f)));
+                    // below -88, -inf too, the reciprocal comes out 0
+                    s[i] = recip_32(1.0f + exp_32(fminf(-l[i], 88.0f)));
                     z += s[i];
                 }
             }
