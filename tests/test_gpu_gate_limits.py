@@ -59,3 +59,31 @@ def test_logistic_scores_far_below_the_rows_largest(N, dtype):
         p = check(l.to(dtype), None, 3, score="sigmoid")
         if low == -INF:
             assert p[9] == 1.0 and np.count_nonzero(p) == 1
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("left", [0, 3, 7, 8, 9, 40])
+@pytest.mark.parametrize("nodes", [False, True])
+@pytest.mark.parametrize("by", ["bias", "logits"])
+def test_few_experts_left_and_preferred_ones(by, nodes, left, score):
+    """Fewer, just as many and a few more experts left than slots, some of them near ties, and
+    biases of +inf: ranks, not the number of experts in sight, decide."""
+    T, N, k = 65, 256, 8
+    g = torch.Generator().manual_seed(left)
+    l = torch.randn(T, N, generator=g)
+    b = torch.randn(N, generator=g) * 0.05
+    on = torch.randperm(N, generator=g)[:left]
+    if left > 1:
+        l[:, on[1]] = l[:, on[0]]                         # equal logits, biases one step apart
+        b[on[1]] = torch.nextafter(b[on[0]], torch.tensor(1.0))
+    off = torch.ones(N, dtype=torch.bool)
+    off[on] = False
+    if by == "bias":
+        b[off] = -INF
+    else:
+        l[:, off] = -INF
+    kw = dict(n_groups=8, topk_groups=4, group_top=2) if nodes else {}
+    check(l, b, k, score=score, renorm=True, **kw)
+    if left > 3:
+        b[on[2:4]] = INF
+        check(l, b, k, score=score, renorm=True, **kw)

@@ -283,19 +283,30 @@ __device__ __forceinline__ double key_value_of(uint64_t k)
     return __longlong_as_double(static_cast<long long>((k >> 63) ? (k & 0x7FFFFFFFFFFFFFFFull) : ~k));
 }
 
-// Whether a >= b are far enough apart to be ordered right (or not comparable:
-// an infinity).  An expert's value is off by at most margin / 2 times 1 + |v|.
+// Whether a >= b are far enough apart to be ordered right.  An expert's value is
+// off by at most margin / 2 times 1 + |v|; an infinity is exact, and apart from
+// every other value (the bound is kept finite), but not from its like.
 template <typename F>
 __device__ __forceinline__ bool apart(F a, F b, F margin)
 {
-    const F size = larger(a < 0 ? -a : a, b < 0 ? -b : b);
-    return !(a - b <= margin * (F(1) + size));
+    const F size = smaller(larger(a < 0 ? -a : a, b < 0 ? -b : b), F(FLT_MAX));
+    return a - b > margin * (F(1) + size);
 }
+
+// A key below which every value is apart from `a` (twice the bound covers a
+// lower value of larger size).  Experts that are switched off lie below it,
+// whatever a is: they come in the order of their indices, which needs no bound.
+__device__ __forceinline__ uint32_t not_apart_key(float a, float margin)
+{
+    const uint32_t k = order_key(a < INFINITY ? a - 2.0f * margin * (1.0f + fabsf(a)) : a);
+    return k > kOffKey ? k : kOffKey + 1;
+}
+__device__ __forceinline__ uint64_t not_apart_key(double, double) { return 0; }   // margin < 0
 
 // The choice: v = s + b of this lane's experts (-inf: switched off), K the key
 // type of F.  Lane j gets the j-th best expert in `mine` and its key in
 // `my_key`, for the `found` best: p.k of them, or with `margin` >= 0 one more,
-// and all (up to 32) that are not apart() from the k-th.  Returns whether a
+// and all (up to 32) that may not be apart() from the k-th.  Returns whether a
 // chosen node's score is too near the first one left out, with sums off by
 // node_margin times their size.
 template <typename F, typename K, int VPL>
@@ -386,7 +397,7 @@ __device__ __forceinline__ bool choose(const RouteParams &p, const F (&v)[VPL],
     }
     my_key = 0;
     mine = 0;
-    K kth = 0;
+    K stop = 0;
     uint32_t gone = 0;
     for (found = 0; found < 32;) {
         const K m = key_max(best);
@@ -400,11 +411,11 @@ __device__ __forceinline__ bool choose(const RouteParams &p, const F (&v)[VPL],
         }
         ++found;
         if (found == p.k) {
-            kth = m;
             if (margin < 0)
                 break;
+            stop = not_apart_key(key_value_of(m), margin);
         }
-        if (found > p.k && apart(key_value_of(kth), key_value_of(m), margin))
+        if (m < stop)
             break;
         const bool won = lane == src;
         gone |= won ? 1u << bi : 0u;
