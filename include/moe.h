@@ -349,8 +349,10 @@ size_t moe_route_workspace_bytes(const moe_route_config *cfg);
  * divided by the sum of the k chosen scores if `renormalize` (0 when all of
  * them are switched off).
  * A logit of -inf (or a bias of -inf) switches the expert off for the token:
- * it ranks behind every other, lowest index first, -inf logits score 0, and a
- * node's score leaves it out; a token without any expert left gets the lowest
+ * it ranks behind every other of the chosen nodes, lowest index first, -inf
+ * logits score 0, and a node's score leaves it out: a node without any expert
+ * left scores 0, so it comes before nodes whose sums are negative (biases that
+ * outweigh their scores); a token without any expert left gets the lowest
  * indices with weight 0 (for a -inf logit) and adds nothing to p_mean (it
  * still takes rows in moe_dispatch).  +inf
  * counts as the largest finite fp32 value.  A NaN logit or bias counts as

@@ -87,3 +87,30 @@ def test_few_experts_left_and_preferred_ones(by, nodes, left, score):
     if left > 3:
         b[on[2:4]] = INF
         check(l, b, k, score=score, renorm=True, **kw)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("group_top", [1, 2, 4, 5])
+@pytest.mark.parametrize("by", ["bias", "logits"])
+def test_a_node_without_experts_scores_zero(by, group_top, score):
+    """Its score is the sum of nothing: behind nodes with positive sums, ahead of negative ones."""
+    T, N, G, k = 33, 64, 8, 6
+    l = torch.randn(T, N, generator=torch.Generator().manual_seed(group_top))
+    for shift in (0.5, -1.5):                             # all sums positive, all negative
+        b = torch.full((N,), shift)
+        b[40:48] += 0.25                                  # the fifth node ahead of the others
+        x = l.clone()
+        if by == "bias":
+            b[16:24] = -INF
+        else:
+            x[:, 16:24] = -INF
+        check(x, b, k, score=score, n_groups=G, topk_groups=1, group_top=group_top)
+        idx, w, _ = run(x, b, k, score=score, n_groups=G, topk_groups=1, group_top=group_top)
+        empty = (idx >= 16) & (idx < 24)
+        assert empty.any() == (shift < 0)
+        if by == "logits":
+            assert np.all(w[empty] == 0)
+        # a very low finite bias in place of -inf keeps the node behind all others
+        b[16:24] = -1e30
+        idx, _, _ = run(l, b, k, score=score, n_groups=G, topk_groups=1, group_top=group_top)
+        assert not ((idx >= 16) & (idx < 24)).any()
