@@ -10,21 +10,29 @@
 namespace moe {
 namespace lin {
 
-// e^(-z^2 / 2) and the normal distribution's Phi(z), fp32, Phi within 1e-7:
-// erfc(x) = (a1 t + .. + a5 t^5) e^(-x^2), t = 1 / (1 + p x), x >= 0
-// (Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26).  It
-// shares its exponential with the density; the library's error function next
-// to an exponential cost twice the instructions, and the element-wise GELU
-// gradient is bound by them (4096 x 4096 bf16: 34 us with it, 28 us so).
+// e^(-z^2 / 2) and the normal distribution's Phi(z), fp32.  For x = |z| and
+// r = 1 / (x + 3), (x + 3) e^(x^2 / 2) Phi(-x) is smooth in t = 1 - 6 r, which
+// runs from -1 at x = 0 to 1; the polynomial is its fit of least relative error
+// over 0 <= x <= 14 (5e-8; weighted least squares on values to 40 digits), with
+// coefficients that fall off, so little is lost to rounding.  Phi is within 2e-7,
+// and below 0 within 1.5e-6 of itself down to -8 (the exponent's rounding grows
+// with z^2).  It shares its exponential with the density; a library's error
+// function next to an exponential costs twice the instructions, and the
+// element-wise GELU gradient is bound by them.
 __device__ __forceinline__ void normal_cdf(float z, float &phi, float &e)
 {
     e = exp_32(-0.5f * z * z);
-    const float t = recip_32(fmaf(0.3275911f * 0.70710678118654752f, fabsf(z), 1.0f));
-    float q = fmaf(1.061405429f, t, -1.453152027f);
-    q = fmaf(q, t, 1.421413741f);
-    q = fmaf(q, t, -0.284496736f);
-    q = fmaf(q, t, 0.254829592f);
-    q *= 0.5f * t * e;
+    const float r = recip_32(fabsf(z) + 3.0f);
+    const float t = fmaf(-6.0f, r, 1.0f);
+    float q = fmaf(-2.66765798e-4f, t, -9.03251872e-4f);
+    q = fmaf(q, t, 1.07603637e-3f);
+    q = fmaf(q, t, 6.92392187e-3f);
+    q = fmaf(q, t, -1.04799354e-2f);
+    q = fmaf(q, t, -4.72561009e-2f);
+    q = fmaf(q, t, 2.30019346e-1f);
+    q = fmaf(q, t, -5.09332299e-1f);
+    q = fmaf(q, t, 7.29083657e-1f);
+    q *= r * e;
     phi = z < 0.0f ? q : 1.0f - q;
 }
 
