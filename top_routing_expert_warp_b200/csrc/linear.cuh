@@ -37,7 +37,8 @@ __device__ __forceinline__ void normal_cdf(float z, float &phi, float &e)
 }
 
 // z kept between lo and hi, a NaN as it is: outside, the functions below are
-// their limits to the last bit, and no product meets an infinity.
+// their limits (what is left of them lies below the smallest normal number times
+// |z|), and no product meets an infinity.  The reciprocal of 1 + e^88 flushes to 0.
 __device__ __forceinline__ float within(float z, float lo, float hi)
 {
     return z < lo ? lo : (z > hi ? hi : z);
@@ -51,7 +52,7 @@ __device__ __forceinline__ float act_fwd(float z)
     if (ACT == MOE_LINEAR_RELU)
         return z < 0.0f ? 0.0f : z;      // a NaN stays one
     if (ACT == MOE_LINEAR_SILU) {
-        z = z < -80.0f ? -80.0f : z;
+        z = z < -88.0f ? -88.0f : z;
         return z * recip_32(1.0f + exp_32(-z));
     }
     if (ACT == MOE_LINEAR_GELU) {
@@ -63,7 +64,7 @@ __device__ __forceinline__ float act_fwd(float z)
     if (ACT == MOE_LINEAR_GELU_TANH) {
         z = z < -20.0f ? -20.0f : z;
         const float u = 0.79788456080286536f * fmaf(0.044715f * z, z * z, z);
-        return z * recip_32(1.0f + exp_32(fminf(-2.0f * u, 80.0f)));
+        return z * recip_32(1.0f + exp_32(fminf(-2.0f * u, 88.0f)));
     }
     return z;
 }
@@ -75,7 +76,7 @@ __device__ __forceinline__ float act_bwd(float z)
     if (ACT == MOE_LINEAR_RELU)
         return z > 0.0f ? 1.0f : 0.0f;
     if (ACT == MOE_LINEAR_SILU) {
-        z = within(z, -80.0f, 80.0f);
+        z = within(z, -88.0f, 88.0f);
         const float s = recip_32(1.0f + exp_32(-z));
         return s * fmaf(z, 1.0f - s, 1.0f);
     }
@@ -88,7 +89,7 @@ __device__ __forceinline__ float act_bwd(float z)
     if (ACT == MOE_LINEAR_GELU_TANH) {
         z = within(z, -20.0f, 20.0f);
         const float u = 0.79788456080286536f * fmaf(0.044715f * z, z * z, z);
-        const float p = recip_32(1.0f + exp_32(fminf(-2.0f * u, 80.0f)));
+        const float p = recip_32(1.0f + exp_32(fminf(-2.0f * u, 88.0f)));
         const float du = 0.79788456080286536f * fmaf(3.0f * 0.044715f * z, z, 1.0f);
         return fmaf(2.0f * z * du, p * (1.0f - p), p);
     }
