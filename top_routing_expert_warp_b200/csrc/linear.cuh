@@ -1,5 +1,5 @@
-// Activations of the dense projections and the element-wise end of a tile,
-// shared by the CUDA-core and the tensor-core kernels.
+// Activations of the dense projections, their slopes, and the arguments of the
+// element-wise end of a tile, shared by the CUDA-core and the tensor-core kernels.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -101,29 +101,17 @@ __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162flo
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
-// act(z + bias) + residual for one element; writes z to preact if wanted.
+// What is done to a sum before it is stored; the kernels apply it to the pieces
+// of a tile that they hold.
 struct Epilogue {
     void *out;               // [rows, ldo]
     int64_t ldo;
     const float *bias;       // [cols] or null
     const void *residual;    // [rows, ldr] of the output type, or null
     int64_t ldr;
-    void *preact;            // [rows, cols] of the operand type, or null
-    int32_t rows, cols;
+    void *preact;            // [rows, cols] of the operand type, or null: sum + bias
+    int32_t cols;
 };
-
-template <int ACT, typename TO, typename TP>
-__device__ __forceinline__ void finish(const Epilogue &ep, int64_t row, int col, float z)
-{
-    if (ep.bias)
-        z += ep.bias[col];
-    if (ep.preact)
-        put(static_cast<TP *>(ep.preact) + row * ep.cols + col, z);
-    float y = act_fwd<ACT>(z);
-    if (ep.residual)
-        y += to_f32(static_cast<const TO *>(ep.residual)[row * ep.ldr + col]);
-    put(static_cast<TO *>(ep.out) + row * ep.ldo + col, y);
-}
 
 // Calls f with the activation as a constant.
 template <typename F>

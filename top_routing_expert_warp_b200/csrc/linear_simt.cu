@@ -551,7 +551,6 @@ lin::Epilogue epilogue_of(const LinearGemm &L)
     ep.residual = L.residual;
     ep.ldr = L.ldr;
     ep.preact = L.preact;
-    ep.rows = static_cast<int32_t>(L.I);
     ep.cols = L.J;
     return ep;
 }

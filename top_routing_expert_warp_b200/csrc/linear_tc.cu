@@ -25,10 +25,11 @@
 // it adds them in slice order and finishes them.  Through global memory with
 // a ticket this took 4-12 us per launch instead of 2.
 //
-// Roles: warp 0 TMA producer, warp 1 MMA issuer, warps 2-9 epilogue (two per
-// TMEM lane quarter, on alternate 32-column steps).  Two accumulators in TMEM:
-// the epilogue of a tile overlaps the products of the next.  Every wait is
-// bounded.
+// Roles: warp 0 TMA producer, warp 1 MMA issuer, the others the epilogue: eight
+// of them, two per TMEM lane quarter on alternate 32-column steps, or in the
+// form with chains sixteen, four per quarter with a quarter of the columns each.
+// Two accumulators in TMEM: the epilogue of a tile overlaps the products of the
+// next.  Every wait is bounded.
 //
 // The tensor cores' fp32 sums are cut (not rounded) at every step, an error that
 // grows with the length of the chain (1e-9 of the norm per k).  So a slice uses
@@ -890,7 +891,6 @@ cudaError_t launch_linear_tc(const LinearGemm &L, cudaStream_t stream)
     p.ep.residual = L.residual;
     p.ep.ldr = L.ldr;
     p.ep.preact = L.preact;
-    p.ep.rows = static_cast<int32_t>(L.I);
     p.ep.cols = L.J;
     p.status = L.status;
     p.first_of_two = L.first_of_two;
