@@ -364,7 +364,7 @@ def _arg(where, device, name, t, code, shape, ld=None, optional=False):
         raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: {name} is missing")
     if type(t) is int:
         return t
-    if t.dtype is not _t.dtype[code]:
+    if t.dtype is not _t.dtype.get(code):      # (None for a type the C call does not know either)
         raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: {name} is {t.dtype}")
     if t.shape != shape:
         raise MoeError(MOE_ERR_INVALID_ARG,
