@@ -433,7 +433,7 @@ size_t moe_linear_workspace_bytes(const moe_linear_config *cfg, int32_t backward
  *   preact   [M, n_out] dtype out or NULL: z, which moe_linear_backward needs
  *            when there is an activation
  * Products are summed in fp32 and the epilogue is computed in fp32 with one
- * rounding to the output type. */
+ * rounding to the output type.  y and preact must not overlap x, W or bias. */
 moe_status moe_linear(const moe_linear_config *cfg, const void *x, const void *W,
                       const float *bias, const void *residual, void *y, void *preact,
                       void *workspace, size_t workspace_bytes, void *stream);

@@ -134,9 +134,9 @@ __device__ __forceinline__ void act_all(float (&v)[8][4])
 // GPU are cut along k; the slices' sums go through the workspace and the last
 // block to finish adds them in slice order (a ticket per tile, which wraps to
 // 0).  Bound by shared memory's read rate (80 % of it) and the fp32 pipes:
-// 1024^3 in 64 us, 2048^3 in 402 us = 43 TFLOP/s, three quarters of what a
-// library product reaches.  8 x 8 outputs per thread read half as much but
-// left too few warps: 61 and 430 us.
+// 1024^3 in 64 us, 2048^3 in 403 us = 43 TFLOP/s (a library product takes 47 and
+// 309 us).  8 x 8 outputs per thread read half as much but left too few warps:
+// 61 and 430 us.
 template <bool P_K, bool Q_K>
 __device__ __forceinline__ void simt_tile(const SimtParams &p)
 {
@@ -441,8 +441,8 @@ __device__ __forceinline__ void store_v(__nv_bfloat16 *p, const float (&v)[V])
 // the unrounded dz, in 32 bits: a warp sums every eighth row of the block's in
 // order, then the eight sums are added in order.  A lane holds V columns (16
 // bytes of the operand type where rows allow it).  Bound by the bytes of dy, z
-// and dz for ReLU (4096 x 4096 bf16 in 15 us), by its instructions for the
-// others (SiLU 20 us, GELU 24 us).
+// and dz for ReLU (4096 x 4096 bf16 in 16 us), by its instructions for the
+// others (SiLU 20 us, GELU 26 us, its tanh form 25 us).
 template <typename T, typename TO, int ACT, int V>
 __global__ void __launch_bounds__(kThreads)
     linear_dz_kernel(const TO *__restrict__ dy, int64_t ldy, const T *__restrict__ z, int64_t M,

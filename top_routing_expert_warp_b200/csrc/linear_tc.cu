@@ -46,9 +46,9 @@
 // What bounds it: large products the tensor cores under the power limit (4096 x
 // 4096 -> 14336 back to back 391 us = 1230 TFLOP/s, a library's product 385 to
 // 391 us; with bias, GELU, residual and saved pre-activations, 350 MB more of
-// traffic, 458 us); short ones the chain of launch, first loads, slices'
+// traffic, 460 to 475 us); short ones the chain of launch, first loads, slices'
 // meeting and stores (16 x 7168 -> 2048 14 us, of it 5 for the weights' bytes;
-// 4096 x 7168 -> 256 fp32 26 us, of it 10 for the rows' bytes: the 96 CTAs that
+// 4096 x 7168 -> 256 fp32 27 us, of it 10 for the rows' bytes: the 96 CTAs that
 // clusters of 6 leave busy have 18 MB in flight).
 #include "common.cuh"
 #include "kernels.h"

@@ -521,13 +521,18 @@ __device__ __noinline__ int order_exact(const RouteParams &p, const void *row, i
     return sorted;
 }
 
-// One warp per token, VPL consecutive experts per lane.  What bounds it is the
-// warps' issue rate (k rounds of a warp maximum, the exponentials), not the
-// bytes; so values are formed and compared in 32 bits, and a token whose
-// decisions hang on differences near the 32-bit error is decided again in 64
-// (all in 64 bits: 44 us at 4096 x 256 with nodes and a bias, now 15; 65536
-// tokens 105 us).  Without a bias and nodes the 32-bit keys are the logits
-// themselves and decide exactly (32771 x 128 bf16, top-1: 14 us).
+// One warp per token, VPL consecutive experts per lane.  What bounds it is not
+// the bytes (4 to 7 % of the copy rate).  A prompt's batch is bound by latency:
+// a token is one long chain (k rounds of a warp maximum, the exponentials, the
+// sums), and 4096 tokens of 256 experts on 444 blocks of 8 warps are two for 544
+// of the warps while the others wait (1500 instructions per token, issued at
+// 0.48 per cycle, a third of the warps active).  Larger and smaller-gated batches
+// come nearer to the issue rate (32771 x 128 top-1: 290 instructions, 0.66 per
+// cycle).  So values are formed and compared in 32 bits, and a token whose
+// decisions hang on differences near the 32-bit error is decided again in 64 (all
+// in 64 bits: 44 us at 4096 x 256 with nodes and a bias, now 16, and 3 for the
+// second launch that adds up p; 65536 tokens 111 and 118 us).  Without a bias and nodes the 32-bit keys are
+// the logits themselves and decide exactly (32771 x 128 bf16, top-1: 15 us).
 template <int VPL, bool BF16, bool SOFTMAX>
 __global__ void __launch_bounds__(kThreads, VPL == 8 ? 3 : 4)
     route_kernel(const __grid_constant__ RouteParams p)
@@ -824,7 +829,7 @@ __device__ __forceinline__ void logistic_pair(float l, float &s, float &om)
 // not underflow.  One warp per token: the logits are read once and the
 // gradient is written once (2 T N values, the bound by bytes), the k chosen
 // experts' gradients a second time by the lanes that hold the slots.  65536 x
-// 256 fp32 in 36 us, 60 % of a plain copy's rate; bound by issue (0.7 per cycle,
+// 256 fp32 in 36 us, 60 % of a plain copy's rate; bound by issue (0.71 per cycle,
 // some 400 instructions per token).
 template <int VPL, bool BF16, bool SOFTMAX>
 __global__ void __launch_bounds__(kThreads, 4)
