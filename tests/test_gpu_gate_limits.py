@@ -114,3 +114,32 @@ def test_a_node_without_experts_scores_zero(by, group_top, score):
         b[16:24] = -1e30
         idx, _, _ = run(l, b, k, score=score, n_groups=G, topk_groups=1, group_top=group_top)
         assert not ((idx >= 16) & (idx < 24)).any()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("nodes", [False, True])
+@pytest.mark.parametrize("N", [64, 128, 256])
+def test_many_equal_experts_before_a_slightly_better_one(N, nodes, score):
+    """The first 40 experts are equal, and later ones better by less than 32 bits of the score show:
+    the better ones are chosen, however many equal ones lie before them."""
+    k = 4
+    l = torch.full((24, N), 0.75)
+    l[0, 50] += 2.0 ** -24                                # one fp32 step
+    l[1, 41:] += 2.0 ** -24
+    l[2] = 20.0                                           # logistic scores of 1 in 32 bits
+    l[2, 45:52] = 22.0
+    l[3, :] = 20.0
+    l[3, 60] = INF
+    l[4, :] = -30.0                                       # beside a bias that dwarfs them
+    l[4, 55] = -29.0
+    l[5, 40:] -= 2.0 ** -24                               # the first ones are the better ones
+    l[7, ::3] = -INF                                      # equal, some off
+    l[8, :] = -INF
+    l[9, 3:40] = -INF
+    l[9, 60] += 2.0 ** -24
+    kw = dict(n_groups=4, topk_groups=3, group_top=2) if nodes else {}
+    zero = torch.zeros(N)
+    later = zero.clone()
+    later[47] = 2.0 ** -30                                # the same by the bias
+    for b in (zero, later, zero - 1.0, later - 1.0, zero + 1e6, torch.where(torch.arange(N) % 5 == 0, -INF, zero)):
+        check(l, b, k, score=score, renorm=True, **kw)

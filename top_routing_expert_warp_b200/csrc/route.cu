@@ -521,6 +521,29 @@ __device__ __noinline__ int order_exact(const RouteParams &p, const void *row, i
     return sorted;
 }
 
+// Whether all experts that are not switched off have one logit and one bias, so
+// that their order is that of their indices in every precision.
+template <int VPL, bool BF16>
+__device__ __noinline__ bool row_tied(const RouteParams &p, const void *row)
+{
+    const int e0 = (threadIdx.x & 31) * VPL;
+    bool ignore = false;
+    float l[VPL], hi = -INFINITY, low = -INFINITY, b_hi = -INFINITY, b_low = -INFINITY;
+    load_logits<VPL, BF16>(row, e0, p.N, p.vec, l);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const float li = clean_logit(l[i], ignore);
+        const float b = e0 + i < p.N ? fmaxf(p.bias[e0 + i], -INFINITY) : -INFINITY;
+        if (li != -INFINITY && b != -INFINITY) {
+            hi = fmaxf(hi, li);
+            low = fmaxf(low, -li);
+            b_hi = fmaxf(b_hi, b);
+            b_low = fmaxf(b_low, -b);
+        }
+    }
+    return warp_max(hi) == -warp_max(low) && warp_max(b_hi) == -warp_max(b_low);
+}
+
 // One warp per token, VPL consecutive experts per lane.  What bounds it is not
 // the bytes (4 to 7 % of the copy rate).  A prompt's batch is bound by latency:
 // a token is one long chain (k rounds of a warp maximum, the exponentials, the
@@ -674,6 +697,9 @@ __global__ void __launch_bounds__(kThreads, VPL == 8 ? 3 : 4)
                             mine = order_exact<BF16>(p, row, mine, found);
                         else
                             exact = true;
+                    } else if (found == 32) {
+                        // equal ones as far as was looked: what lies behind may differ
+                        exact = !row_tied<VPL, BF16>(p, row);
                     }
                 }
             }
