@@ -7,7 +7,9 @@ import re
 import pytest
 import torch
 
+import synth
 import top_routing_expert_warp_b200 as moe
+from gpu_util import LayerRun, upload_inputs
 from top_routing_expert_warp_b200 import build as moe_build
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -121,6 +123,61 @@ def test_captured_graphs_of_two_sizes_share_a_workspace():
         graph.replay()
         torch.cuda.synchronize()
         for a, b in zip(out, want[i]):
+            assert torch.equal(a, b)
+
+
+LAYERS = {
+    "fp32": synth.TINY_F32,
+    "fp32-capacity": synth.TINY_F32.with_(capacity_factor=0.6, seed=41),
+    "top2": synth.MIXTRAL.with_(T=300, d=256, H=384),
+    "drops": synth.SWITCH.with_(T=1000, d=128, H=256),
+    "fallback": synth.SWITCH.with_(T=700, d=128, H=256, overflow="fallback", capacity_factor=0.5, seed=42),
+    "fp8-shared": synth.DEEPSEEK.with_(T=200, d=256, H=128, H_shared=128),
+    "fp8": synth.DEEPSEEK.with_(T=300, d=272, H=192, H_shared=0, seed=31),
+}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", list(LAYERS))
+def test_layers_do_not_read_what_others_left(name):
+    """Any bytes behind the head (NaN patterns among them) change nothing."""
+    wl = LAYERS[name]
+    dev, _ = upload_inputs(wl)
+    run = LayerRun(wl, dev)
+    outs = lambda: [t.clone() for t in (run(), run.topk_idx, run.topk_w, run.counts, run.f,  # noqa: E731
+                                        run.p_mean, run.aux)]
+    want = outs()
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for fill in (None, 255, 127):
+        if fill is None:
+            run.ws[HEAD:].random_(0, 256, generator=g)
+        else:
+            run.ws[HEAD:] = fill
+        for a, b in zip(outs(), want):
+            assert torch.equal(a, b)
+    assert run.check_status()[0] == moe.MOE_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_the_gate_and_projections_do_not_read_what_others_left(dt):
+    cfg = moe.make_linear_config(300, 1032, 137, dtype=dt)
+    ws = moe.linear_workspace(cfg)
+    want = grads(cfg, ws, dt, 5)
+    rc = moe.make_route_config(5000, 96, 4, score="sigmoid")
+    l = torch.randn(5000, 96, generator=torch.Generator().manual_seed(2)).cuda()
+
+    def route(w):
+        idx, tw = torch.empty(5000, 4, dtype=torch.int32, device="cuda"), torch.empty(5000, 4, device="cuda")
+        p = torch.empty(96, device="cuda")
+        moe.moe_route(rc, l, None, idx, tw, p, w)
+        return [idx, tw, p]
+    rws = moe.route_workspace(rc)
+    want_r = route(rws)
+    for fill in (255, 127):
+        ws[HEAD:] = fill
+        rws[HEAD:] = fill
+        for a, b in zip(grads(cfg, ws, dt, 5) + route(rws), want + want_r):
             assert torch.equal(a, b)
 
 
