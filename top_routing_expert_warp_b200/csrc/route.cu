@@ -434,12 +434,39 @@ __device__ __forceinline__ bool choose(const RouteParams &p, const F (&v)[VPL],
     return near;
 }
 
+// Whether all experts that are not switched off have one logit and one bias, so
+// that their order is that of their indices in every precision.
+template <int VPL, bool BF16>
+__device__ __forceinline__ bool row_tied(const RouteParams &p, const void *row)
+{
+    const int e0 = (threadIdx.x & 31) * VPL;
+    bool ignore = false;
+    float l[VPL], hi = -INFINITY, low = -INFINITY, b_hi = -INFINITY, b_low = -INFINITY;
+    load_logits<VPL, BF16>(row, e0, p.N, p.vec, l);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const float li = clean_logit(l[i], ignore);
+        const float b = e0 + i < p.N ? fmaxf(p.bias[e0 + i], -INFINITY) : -INFINITY;
+        if (li != -INFINITY && b != -INFINITY) {
+            hi = fmaxf(hi, li);
+            low = fmaxf(low, -li);
+            b_hi = fmaxf(b_hi, b);
+            b_low = fmaxf(b_low, -b);
+        }
+    }
+    return warp_max(hi) == -warp_max(low) && warp_max(b_hi) == -warp_max(b_low);
+}
+
 // The choice in 64 bits, from the logits: the index of lane j's slot (lanes
 // below k).  Taken for tokens whose 32-bit values are too near one another.
-// s_val: doubles of this warp.
+// s_val: doubles of this warp.  A token whose experts are all equal keeps its slots
+// in `tied` (if not negative).
 template <int VPL, bool BF16, bool SOFTMAX>
-__device__ __noinline__ int choose_exact(const RouteParams &p, const void *row, double *s_val)
+__device__ __noinline__ int choose_exact(const RouteParams &p, const void *row, double *s_val,
+                                         int tied)
 {
+    if (__any_sync(kAll, tied >= 0) && row_tied<VPL, BF16>(p, row))
+        return tied;
     const int lane = threadIdx.x & 31;
     const int e0 = lane * VPL;
     bool ignore = false;
@@ -521,35 +548,12 @@ __device__ __noinline__ int order_exact(const RouteParams &p, const void *row, i
     return sorted;
 }
 
-// Whether all experts that are not switched off have one logit and one bias, so
-// that their order is that of their indices in every precision.
-template <int VPL, bool BF16>
-__device__ __noinline__ bool row_tied(const RouteParams &p, const void *row)
-{
-    const int e0 = (threadIdx.x & 31) * VPL;
-    bool ignore = false;
-    float l[VPL], hi = -INFINITY, low = -INFINITY, b_hi = -INFINITY, b_low = -INFINITY;
-    load_logits<VPL, BF16>(row, e0, p.N, p.vec, l);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        const float li = clean_logit(l[i], ignore);
-        const float b = e0 + i < p.N ? fmaxf(p.bias[e0 + i], -INFINITY) : -INFINITY;
-        if (li != -INFINITY && b != -INFINITY) {
-            hi = fmaxf(hi, li);
-            low = fmaxf(low, -li);
-            b_hi = fmaxf(b_hi, b);
-            b_low = fmaxf(b_low, -b);
-        }
-    }
-    return warp_max(hi) == -warp_max(low) && warp_max(b_hi) == -warp_max(b_low);
-}
-
 // One warp per token, VPL consecutive experts per lane.  What bounds it is not
 // the bytes (4 to 7 % of the copy rate).  A prompt's batch is bound by latency:
 // a token is one long chain (k rounds of a warp maximum, the exponentials, the
 // sums), and 4096 tokens of 256 experts on 444 blocks of 8 warps are two for 544
 // of the warps while the others wait (1500 instructions per token, issued at
-// 0.48 per cycle, a third of the warps active).  Larger and smaller-gated batches
+// 0.47 to 0.48 per cycle, a third of the warps active).  Larger and smaller-gated batches
 // come nearer to the issue rate (32771 x 128 top-1: 290 instructions, 0.66 per
 // cycle).  So values are formed and compared in 32 bits, and a token whose
 // decisions hang on differences near the 32-bit error is decided again in 64 (all
@@ -673,6 +677,7 @@ __global__ void __launch_bounds__(kThreads, VPL == 8 ? 3 : 4)
                 le = key_value(won);
         } else {
             bool exact = tiny;
+            int tied = -1;
             if (!exact) {
 #pragma unroll
                 for (int i = 0; i < VPL; ++i)
@@ -699,12 +704,13 @@ __global__ void __launch_bounds__(kThreads, VPL == 8 ? 3 : 4)
                             exact = true;
                     } else if (found == 32) {
                         // equal ones as far as was looked: what lies behind may differ
-                        exact = !row_tied<VPL, BF16>(p, row);
+                        exact = true;
+                        tied = mine;
                     }
                 }
             }
             if (exact)
-                mine = choose_exact<VPL, BF16, SOFTMAX>(p, row, s_val[warp]);
+                mine = choose_exact<VPL, BF16, SOFTMAX>(p, row, s_val[warp], tied);
             bool ignore = false;
             if (lane < k)
                 le = clean_logit(load_logit<BF16>(row, mine), ignore);
